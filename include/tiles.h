@@ -457,6 +457,139 @@ tiles_status_t tiles_kv8_from_bf16(const tiles_model_desc *desc, const void *k_b
                                    int32_t n_pos, void *k8, void *v8, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* Paged KV cache: many sequences in one pool of pages, the attention over it, */
+/* and the pages' life.                                                        */
+/*
+ * The pages' own cache is one dense block per sequence ("History and roadmap",
+ * "M8 so far": KV caches of one sequence); these operators have no counterpart
+ * there. A cache holds n_seqs sequences (rows). Position t of row s lies in
+ * page tables[s][t / page_size] at offset t % page_size; -1 means no page.
+ * Pages may be shared by rows (tiles_paged_fork): refs counts their holders.
+ *
+ * All buffers are the caller's, on one device:
+ *   k, v    tiles_paged_layout.k_bytes / v_bytes, 16-byte aligned:
+ *           TILES_KV_BF16: values [n_layers][n_pages][n_kv_heads][page_size][head_dim];
+ *           TILES_KV_INT8: codes int8 of that shape, and at k_scale_off /
+ *           v_scale_off the FP32 scales [n_layers][n_pages][n_kv_heads][page_size].
+ *           A row is quantized as TILES_KV_INT8 states, keys after subtracting
+ *           k_shift where one is given.
+ *   tables  int32 [n_seqs][table_width]; lens int32 [n_seqs]
+ *   state   state_bytes: word 0 the status (read by tiles_paged_status), words
+ *           16 .. 16 + n_pages - 1 the reference counts, the rest working memory
+ *   k_shift float [n_layers][n_kv_heads][head_dim] or NULL (INT8 only): the key
+ *           shift of every row of the cache. Attention never needs it (it moves
+ *           all scores of a query alike).
+ * The calls read lens, tables and the reference counts on the device: none
+ * synchronises, none allocates, and all can be captured into a graph. Calls on
+ * one cache must be ordered (one stream, or events). Device-side faults (a page
+ * id out of range, too few free pages, a bad row) are recorded in the state's
+ * status word; the access is skipped.
+ */
+typedef struct {
+    int32_t n_layers, n_kv_heads, head_dim; /* head_dim 64 or 128                     */
+    int32_t page_size;                      /* 16, 32, 64 or 128                      */
+    int32_t n_pages, n_seqs, table_width;   /* table_width: pages a row can hold      */
+    int32_t kv_format;                      /* TILES_KV_BF16 or TILES_KV_INT8         */
+} tiles_paged_desc;
+
+typedef struct {
+    int64_t k_bytes, v_bytes;         /* sizes of the two pools                       */
+    int64_t k_scale_off, v_scale_off; /* INT8: where the scales begin; BF16: 0        */
+    int64_t state_bytes;
+} tiles_paged_layout;
+
+typedef struct {
+    tiles_paged_desc desc;
+    void *k, *v;
+    int32_t *tables, *lens, *state;
+    const float *k_shift;
+} tiles_paged_cache;
+
+/* Sizes and offsets from desc alone (host only). Errors: INVALID_ARG (null,
+ * non-positive dimension, unknown format), UNSUPPORTED (head_dim, page_size, or
+ * a pool of 2^31 or more (layer, page, head) blocks). */
+tiles_status_t tiles_paged_get_layout(const tiles_paged_desc *desc, tiles_paged_layout *out);
+
+/* Empties the cache: tables -1, lens 0, reference counts and status 0. The
+ * pools are left as they are. Errors of this and the calls below: INVALID_ARG
+ * (null or misaligned buffer, bad option), UNSUPPORTED (as above), CUDA. */
+tiles_status_t tiles_paged_reset(const tiles_paged_cache *cache, void *stream);
+
+/* Sets row lengths: new_lens (device, [n_seqs]); a negative entry leaves the
+ * row alone.
+ *   - Rows that shrink (to 0: the sequence ends) let go of every page behind
+ *     the new end.
+ *   - Then rows that grow get what positions len .. new_len - 1 need: the lowest
+ *     free page for each missing one (rows in order), and a page of their own
+ *     for one that is shared, with the positions before len copied in all layers
+ *     (copy-on-write). Where every holder of a shared page grows in the same
+ *     call, the lowest row keeps it and the others copy.
+ * Growth is all or nothing: with too few free pages no row grows and the status
+ * is TILES_ERR_CAPACITY. new_len > table_width * page_size is recorded as
+ * TILES_ERR_DEVICE_BOUNDS and leaves the row alone. */
+tiles_status_t tiles_paged_resize(const tiles_paged_cache *cache, const int32_t *new_lens, void *stream);
+
+/* Row s becomes a copy of row src_rows[s] (device, [n_seqs]; negative: row s is
+ * left alone): same length, same pages, each held once more. Nothing is copied
+ * until a holder grows. Row s must be empty and src_rows[s] another row that
+ * is not itself the target of a fork in this call; otherwise the row is left
+ * alone and the status is TILES_ERR_DEVICE_BOUNDS. */
+tiles_status_t tiles_paged_fork(const tiles_paged_cache *cache, const int32_t *src_rows, void *stream);
+
+/* Lets go of the pages that no later token can see under `window` >= 1 and
+ * `sinks` >= 0 (see tiles_paged_attention): those whose positions are all >=
+ * sinks and <= len - window. Their table entries become -1; lengths stay. A row
+ * must not shrink afterwards below its length at this call, and later attention
+ * must use no larger window and no more sinks. */
+tiles_status_t tiles_paged_trim(const tiles_paged_cache *cache, int32_t window, int32_t sinks, void *stream);
+
+/* Moves the live pages (reference count > 0) to the front of the pool, 0 ..
+ * n_live - 1: the i-th live page with an id >= n_live goes to the i-th free id
+ * below it, in every layer; tables and reference counts follow. */
+tiles_status_t tiles_paged_compact(const tiles_paged_cache *cache, void *stream);
+
+/* Writes the K and V rows of new tokens of one layer. Row s has tokens
+ * cu_tokens[s] .. cu_tokens[s + 1] - 1 (n_s of them) at positions lens[s] - n_s
+ * .. lens[s] - 1 (resize first). cu_tokens: device, [n_seqs + 1], ascending from
+ * 0, or NULL: one token a row (n_tokens == n_seqs; rows of length 0 have none).
+ * Tokens from cu_tokens[n_seqs] on are padding and left alone, and so are
+ * positions below 0. k, v: BF16, token i of head h at i * k_stride_token +
+ * h * k_stride_head elements, head_dim contiguous; pointers 16-byte aligned and
+ * strides multiples of 8. A row of a dense cache [n_kv][max_pos][d] is moved
+ * into pages with strides (d, max_pos * d). */
+tiles_status_t tiles_paged_append(const tiles_paged_cache *cache, int32_t layer, const void *k, int64_t k_stride_token,
+                                  int64_t k_stride_head, const void *v, int64_t v_stride_token,
+                                  int64_t v_stride_head, const int32_t *cu_tokens, int32_t n_tokens, void *stream);
+
+/* Attention of new tokens over their rows' pages in one layer. Tokens as for
+ * tiles_paged_append; token i of row s is at position p = lens[s] - n_s + i and
+ * sees position t <= p when window == 0, or t > p - window, or t < sinks:
+ *   out = sum_t softmax_t(scale q . K_t) V_t,   0 where it sees nothing.
+ * Positions that it does not see (behind the end, masked, missing pages) have
+ * no influence, whatever their bytes. Query head h reads KV head h / (n_q_heads
+ * / n_kv_heads); up to 16 query heads a KV head. q, out: BF16, strides as for
+ * append (out must not overlap q). max_tokens: a bound on n_s (a row with more
+ * is recorded as TILES_ERR_DEVICE_BOUNDS and skipped). Softmax statistics and
+ * sums are FP32.
+ * workspace: device, 16-byte aligned, tiles_paged_workspace_bytes of it, any
+ * contents; calls that overlap in time must not share it. Errors also:
+ * CAPACITY (workspace too small). */
+tiles_status_t tiles_paged_attention(const tiles_paged_cache *cache, int32_t layer, int32_t n_q_heads, const void *q,
+                                     int64_t q_stride_token, int64_t q_stride_head, void *out,
+                                     int64_t out_stride_token, int64_t out_stride_head, const int32_t *cu_tokens,
+                                     int32_t n_tokens, int32_t max_tokens, float scale, int32_t window,
+                                     int32_t sinks, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace of tiles_paged_attention for up to n_tokens tokens, on the current
+ * device. Errors: as tiles_paged_get_layout, CUDA. */
+tiles_status_t tiles_paged_workspace_bytes(const tiles_paged_desc *desc, int32_t n_q_heads, int32_t max_tokens,
+                                           int64_t *bytes);
+
+/* Synchronises `stream`, reads the cache's status word and clears it: TILES_OK,
+ * TILES_ERR_DEVICE_BOUNDS, TILES_ERR_CAPACITY, TILES_ERR_TIMEOUT or CUDA. */
+tiles_status_t tiles_paged_status(const tiles_paged_cache *cache, void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* Measurement helpers.                                                       */
 
 /* Device-to-device copy of `bytes` (multiple of 16, both pointers 16-byte

@@ -98,6 +98,19 @@ class KV8Layout(ctypes.Structure):
                [("pos_stride", ctypes.c_int32)]
 
 
+class PagedDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n_layers", "n_kv_heads", "head_dim", "page_size", "n_pages", "n_seqs", "table_width", "kv_format")]
+
+
+class PagedLayout(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("k_bytes", "v_bytes", "k_scale_off", "v_scale_off", "state_bytes")]
+
+
+class PagedCacheView(ctypes.Structure):
+    _fields_ = [("desc", PagedDesc)] + [(n, ctypes.c_void_p) for n in ("k", "v", "tables", "lens", "state", "k_shift")]
+
+
 class Task(ctypes.Structure):
     _fields_ = [("op", ctypes.c_uint8), ("phase_kind", ctypes.c_uint8), ("layer", ctypes.c_uint16),
                 ("begin", ctypes.c_uint32), ("end", ctypes.c_uint32),
@@ -113,7 +126,10 @@ EXPORTS = ("tiles_plan_create", "tiles_plan_destroy", "tiles_decode", "tiles_dec
            "tiles_schedule_validate", "tiles_schedule_tasks", "tiles_schedule_cta_bytes",
            "tiles_schedule_destroy", "tiles_copy_bw", "tiles_barrier_cost", "tiles_plan_set_trace",
            "tiles_decode_noalloc", "tiles_quantize_rows_int8", "tiles_schedule_get_info",
-           "tiles_forward", "tiles_verify", "tiles_kv8_get_layout", "tiles_kv8_from_bf16")
+           "tiles_forward", "tiles_verify", "tiles_kv8_get_layout", "tiles_kv8_from_bf16",
+           "tiles_paged_get_layout", "tiles_paged_reset", "tiles_paged_resize", "tiles_paged_fork",
+           "tiles_paged_trim", "tiles_paged_compact", "tiles_paged_append", "tiles_paged_attention",
+           "tiles_paged_workspace_bytes", "tiles_paged_status")
 MAX_FORWARD_TOKENS = 256
 
 _lib_handle = None
@@ -174,6 +190,22 @@ def _lib():
         L.tiles_kv8_get_layout.restype = st
         L.tiles_kv8_from_bf16.argtypes = [ctypes.POINTER(ModelDesc), vp, vp, i32, vp, vp, vp]
         L.tiles_kv8_from_bf16.restype = st
+        pc = ctypes.POINTER(PagedCacheView)
+        f32 = ctypes.c_float
+        L.tiles_paged_get_layout.argtypes = [ctypes.POINTER(PagedDesc), ctypes.POINTER(PagedLayout)]
+        L.tiles_paged_reset.argtypes = [pc, vp]
+        L.tiles_paged_resize.argtypes = [pc, vp, vp]
+        L.tiles_paged_fork.argtypes = [pc, vp, vp]
+        L.tiles_paged_trim.argtypes = [pc, i32, i32, vp]
+        L.tiles_paged_compact.argtypes = [pc, vp]
+        L.tiles_paged_append.argtypes = [pc, i32, vp, i64, i64, vp, i64, i64, vp, i32, vp]
+        L.tiles_paged_attention.argtypes = [pc, i32, i32, vp, i64, i64, vp, i64, i64, vp, i32, i32, f32, i32, i32,
+                                            vp, i64, vp]
+        L.tiles_paged_workspace_bytes.argtypes = [ctypes.POINTER(PagedDesc), i32, i32, ctypes.POINTER(i64)]
+        L.tiles_paged_status.argtypes = [pc, vp]
+        for n in EXPORTS:
+            if n.startswith("tiles_paged_"):
+                getattr(L, n).restype = st
         L.tiles_barrier_cost.argtypes = [i32, i32, ctypes.POINTER(ctypes.c_double)]
         L.tiles_barrier_cost.restype = st
         _lib_handle = L
@@ -239,6 +271,211 @@ class KV8Cache:
                 "mu": part(kb, lay["k_mu_off"], Z * hd, np.float32, (Z, hd)),
                 "vq": part(vb, 0, Z * hd * mp, np.int8, (Z, hd, mp)),
                 "vs": part(vb, lay["v_scale_off"], Z * mp, np.float32, (Z, mp))}
+
+
+# ------------------------------------------------------------------ paged KV cache
+def paged_desc(desc: ModelDesc, n_pages: int, page_size: int = 16, n_seqs: int = 1, max_len: int | None = None,
+               kv_format: int = KV_BF16) -> PagedDesc:
+    """The description of a paged cache for a model's layers, KV heads and head_dim."""
+    max_len = desc.max_pos if max_len is None else int(max_len)
+    return PagedDesc(n_layers=desc.n_layers, n_kv_heads=desc.n_kv_heads, head_dim=desc.head_dim, page_size=page_size,
+                     n_pages=n_pages, n_seqs=n_seqs, table_width=-(-max_len // max(1, page_size)), kv_format=kv_format)
+
+
+def paged_layout(pdesc: PagedDesc) -> dict:
+    """Sizes and offsets of a paged cache's buffers (no GPU)."""
+    lay = PagedLayout()
+    _check(_lib().tiles_paged_get_layout(ctypes.byref(pdesc), ctypes.byref(lay)), "tiles_paged_get_layout")
+    return {n: getattr(lay, n) for n, _ in lay._fields_}
+
+
+class PagedKV:
+    """A paged KV cache of n_seqs sequences (rows) that share one pool of pages
+    (tiles_paged_cache): one pool a layer for K and V each, a page table and a
+    length per row, a reference count per page.
+
+    ``resize`` gives and takes pages, ``fork`` shares a row's, ``trim`` drops what
+    a window no longer sees, ``compact`` closes gaps; ``append`` writes a layer's
+    new K/V rows and ``attention`` reads them. All run on the device and can be
+    captured; order them on one stream. ``check`` raises on what they recorded
+    there (a bad page, too few pages).
+
+    ``k``, ``v``, ``tables``, ``lens``: existing CUDA buffers to use as they are
+    (pools of the layout's size; tables int32 [n_seqs][table_width]; lens int32
+    [n_seqs]; then set ``refs`` too if pages are to be managed here); without
+    them the cache makes its own, empty. ``k_shift``: float32
+    [n_layers][n_kv_heads][head_dim] (INT8 only), subtracted from each appended
+    key. Attributes of the same names are the tensors; ``refs`` is the view of
+    the reference counts."""
+
+    def __init__(self, desc: ModelDesc, n_pages: int, page_size: int = 16, n_seqs: int = 1,
+                 max_len: int | None = None, kv_format: int = KV_BF16, k_shift=None, device="cuda",
+                 k=None, v=None, tables=None, lens=None):
+        import torch
+        self.pdesc = d = paged_desc(desc, n_pages, page_size, n_seqs, max_len, kv_format)
+        self.layout = lay = paged_layout(d)
+        self.device = torch.device(device)
+        if self.device.index is None and self.device.type == "cuda":
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.state = torch.zeros(lay["state_bytes"] // 4, dtype=torch.int32, device=self.device)
+
+        def pool(t, n):
+            if t is None:
+                return torch.zeros(n, dtype=torch.uint8, device=self.device)
+            if t.device != self.device or not t.is_contiguous() or t.numel() * t.element_size() < n:
+                raise TilesError(-1, "PagedKV: a pool is contiguous, on the cache's device and of the layout's size")
+            return t
+
+        def ints(t, shape, fill):
+            if t is None:
+                return torch.full(shape, fill, dtype=torch.int32, device=self.device)
+            if t.device != self.device or t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+                raise TilesError(-1, f"PagedKV: tables and lens are contiguous int32 of shape {shape}")
+            return t
+        self.k, self.v = pool(k, lay["k_bytes"]), pool(v, lay["v_bytes"])
+        self.tables = ints(tables, (n_seqs, d.table_width), -1)
+        self.lens = ints(lens, (n_seqs,), 0)
+        if k_shift is not None and (k_shift.device != self.device or k_shift.dtype != torch.float32 or
+                                    not k_shift.is_contiguous() or
+                                    k_shift.numel() != d.n_layers * d.n_kv_heads * d.head_dim):
+            raise TilesError(-1, "PagedKV: k_shift is contiguous float32 [n_layers][n_kv_heads][head_dim]")
+        self.k_shift = k_shift
+        self.refs = self.state[16:16 + n_pages]
+        self._view = PagedCacheView(desc=d, **{n: None if t is None else t.data_ptr() for n, t in (
+            ("k", self.k), ("v", self.v), ("tables", self.tables), ("lens", self.lens), ("state", self.state),
+            ("k_shift", k_shift))})
+        self._ref = ctypes.byref(self._view)
+        self._ws_bytes = {}
+
+    def _values(self, buf, off: int):
+        import torch
+        d = self.pdesc
+        shape = (d.n_layers, d.n_pages, d.n_kv_heads, d.page_size, d.head_dim)
+        n = d.n_layers * d.n_pages * d.n_kv_heads * d.page_size
+        flat = buf.view(torch.uint8).flatten()
+        if d.kv_format == KV_INT8:
+            return (flat[:n * d.head_dim].view(torch.int8).view(shape),
+                    flat[off:off + 4 * n].view(torch.float32).view(shape[:4]))
+        return flat[:2 * n * d.head_dim].view(torch.bfloat16).view(shape), None
+
+    def key_pool(self):
+        """(values BF16 or codes int8 [n_layers][n_pages][n_kv_heads][page_size][head_dim],
+        scales float32 or None): views of the pool."""
+        return self._values(self.k, self.layout["k_scale_off"])
+
+    def value_pool(self):
+        return self._values(self.v, self.layout["v_scale_off"])
+
+    def _on(self, stream):
+        """The call's stream (default: torch's current one), once the cache's device is the current one."""
+        import torch
+        if self.device.index != torch.cuda.current_device():
+            raise TilesError(-4, "PagedKV: the cache lies on another device than the current one")
+        return ctypes.c_void_p((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+
+    def _rows(self, t, what: str):
+        import torch
+        if t.dtype != torch.int32 or t.device != self.device or t.numel() != self.pdesc.n_seqs or not t.is_contiguous():
+            raise TilesError(-1, f"{what}: int32 [n_seqs] on the cache's device")
+        return t.data_ptr()
+
+    def _cu(self, t, n_tokens: int, what: str):
+        import torch
+        if t is None:
+            return None
+        if t.dtype != torch.int32 or t.device != self.device or t.numel() != self.pdesc.n_seqs + 1 or \
+                not t.is_contiguous():
+            raise TilesError(-1, f"{what}: cu_tokens is int32 [n_seqs + 1] on the cache's device")
+        return t.data_ptr()
+
+    def _heads(self, t, what: str, heads: int | None = None):
+        import torch
+        if t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != self.device or \
+                t.shape[2] != self.pdesc.head_dim or (t.stride(2) != 1 and t.numel()) or \
+                (heads is not None and t.shape[1] != heads):
+            raise TilesError(-1, f"{what}: bfloat16 [tokens][heads][head_dim], head_dim contiguous, on the cache's device")
+        return t.data_ptr()
+
+    def reset(self, stream=None) -> None:
+        """Empties the cache: no pages held, all lengths 0."""
+        _check(_lib().tiles_paged_reset(self._ref, self._on(stream)), "tiles_paged_reset")
+
+    def resize(self, new_lens, stream=None) -> None:
+        """Sets row lengths (int32 CUDA tensor [n_seqs]; negative: leave the row): pages are taken
+        from the pool, given back, and copied where a growing row would write into a shared one."""
+        _check(_lib().tiles_paged_resize(self._ref, self._rows(new_lens, "tiles_paged_resize"), self._on(stream)),
+               "tiles_paged_resize")
+
+    def fork(self, src_rows, stream=None) -> None:
+        """Makes each empty row s with src_rows[s] >= 0 (int32 CUDA tensor [n_seqs]) share that row's pages."""
+        _check(_lib().tiles_paged_fork(self._ref, self._rows(src_rows, "tiles_paged_fork"), self._on(stream)),
+               "tiles_paged_fork")
+
+    def trim(self, window: int, sinks: int = 0, stream=None) -> None:
+        """Gives back the pages that no later token sees under this window and these sink positions."""
+        _check(_lib().tiles_paged_trim(self._ref, window, sinks, self._on(stream)), "tiles_paged_trim")
+
+    def compact(self, stream=None) -> None:
+        """Moves the pages in use to the front of the pool."""
+        _check(_lib().tiles_paged_compact(self._ref, self._on(stream)), "tiles_paged_compact")
+
+    def append(self, layer: int, k, v, cu_tokens=None, stream=None) -> None:
+        """Writes new K/V rows of a layer (BF16 CUDA tensors [tokens][n_kv_heads][head_dim], any token
+        and head strides): row s has tokens cu_tokens[s] .. cu_tokens[s + 1] - 1 (int32 CUDA tensor, or
+        None: one token a row) at its last positions."""
+        n = k.shape[0]
+        h = self.pdesc.n_kv_heads
+        kp, vp = self._heads(k, "tiles_paged_append", h), self._heads(v, "tiles_paged_append", h)
+        if v.shape[0] != n:
+            raise TilesError(-1, "tiles_paged_append: k and v have the same tokens")
+        _check(_lib().tiles_paged_append(self._ref, layer, kp, k.stride(0), k.stride(1), vp, v.stride(0), v.stride(1),
+                                         self._cu(cu_tokens, n, "tiles_paged_append"), n, self._on(stream)),
+               "tiles_paged_append")
+
+    def workspace_bytes(self, n_q_heads: int, max_tokens: int = 1) -> int:
+        """Bytes of workspace that attention needs for rows of up to max_tokens tokens."""
+        key = (n_q_heads, max_tokens)
+        if key not in self._ws_bytes:
+            b = ctypes.c_int64()
+            _check(_lib().tiles_paged_workspace_bytes(ctypes.byref(self.pdesc), n_q_heads, max_tokens,
+                                                      ctypes.byref(b)), "tiles_paged_workspace_bytes")
+            self._ws_bytes[key] = b.value
+        return self._ws_bytes[key]
+
+    def attention(self, layer: int, q, out, cu_tokens=None, max_tokens: int = 1, scale: float | None = None,
+                  window: int = 0, sinks: int = 0, workspace=None, stream=None) -> None:
+        """out = softmax attention of the queries q (BF16 CUDA tensor [tokens][n_q_heads][head_dim]; out
+        likewise) over their rows' positions up to their own, within `window` (0: all) and the first
+        `sinks`. cu_tokens as for append; max_tokens: a bound on a row's tokens; scale: default
+        head_dim ** -0.5. workspace: a uint8 CUDA tensor of workspace_bytes (default: one is taken from
+        PyTorch's allocator for the call)."""
+        import torch
+        n, heads = q.shape[0], q.shape[1]
+        qp, op = self._heads(q, "tiles_paged_attention"), self._heads(out, "tiles_paged_attention", heads)
+        if out.shape[0] != n:
+            raise TilesError(-1, "tiles_paged_attention: q and out have the same tokens")
+        st = self._on(stream)
+        if workspace is None:
+            need = self.workspace_bytes(heads, max_tokens)
+            if stream is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            else:
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise TilesError(-1, "tiles_paged_attention: the workspace is contiguous, on the cache's device")
+        _check(_lib().tiles_paged_attention(
+            self._ref, layer, heads, qp, q.stride(0), q.stride(1), op, out.stride(0), out.stride(1),
+            self._cu(cu_tokens, n, "tiles_paged_attention"), n, max_tokens,
+            self.pdesc.head_dim ** -0.5 if scale is None else scale, window, sinks, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), st), "tiles_paged_attention")
+
+    def status(self, stream=None) -> int:
+        """Synchronises and returns (and clears) what the calls recorded on the device."""
+        return _lib().tiles_paged_status(self._ref, self._on(stream))
+
+    def check(self, stream=None) -> None:
+        _check(self.status(stream), "tiles_paged_status")
 
 
 # ------------------------------------------------------------------ schedule (host only)

@@ -1,0 +1,93 @@
+// The paged KV cache's internals shared by its page management (paged_cache.cu)
+// and its attention (paged_attn.cu, paged_attn_tc.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "tiles_internal.h"
+
+namespace tiles {
+namespace paged {
+
+// int32 words of the state buffer: the status word, then (at kStateRefs) the
+// reference counts and working memory of n_pages words each (writers, lowest,
+// copy sources, copy targets, free list), then n_seqs words (pages a row needs)
+constexpr int kStateStatus = 0, kStateCopies = 1, kStateRefs = 16;
+constexpr int kStateArrays = 6;
+
+// device status bits beyond kDevTimeout and kDevBounds
+constexpr uint32_t kDevNoPages = 4u;
+
+// A cache as the kernels see it (one layer's pools for append and attention).
+struct View {
+    uint8_t *k, *v;      // pools of layer 0, or of the call's layer
+    float *ks, *vs;      // INT8: scales, likewise
+    int32_t *tables, *lens, *state;
+    const float *k_shift;  // of the call's layer, or null
+    int n_layers, nkv, d, ps, n_pages, n_seqs, width, i8;
+};
+
+struct AttnParams {
+    View c;
+    const uint16_t *q;
+    uint16_t *out;
+    long long q_t, q_h, o_t, o_h;  // strides in elements
+    const int32_t *cu;             // null: one token a row
+    int n_tokens, max_tokens, G;
+    float scale_log2;              // scale * log2(e): the softmax runs on powers of two
+    int window, sinks;
+    float *ws;
+    int ctas;                      // CTAs that share the work
+};
+
+// Row s's tokens in the call (first token, count) and its length; a row that
+// breaks the rules (token offsets out of order or range, more than max_tokens)
+// has no tokens, and a length beyond the table is cut to it: *bad says so.
+struct RowSpan {
+    int t0, n, len;
+};
+__device__ __forceinline__ RowSpan row_span(const AttnParams &p, int s, bool *bad) {
+    RowSpan r;
+    int len = __ldg(p.c.lens + s);
+    if (p.cu) {
+        const int a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1);
+        r.t0 = a;
+        r.n = b - a;
+        if (a < 0 || b < a || b > p.n_tokens || r.n > p.max_tokens) {
+            *bad = true;
+            r.t0 = r.n = 0;
+        }
+    } else {
+        r.t0 = s;
+        r.n = 1;
+    }
+    const int cap = p.c.width * p.c.ps;
+    if (len < 0 || len > cap) {
+        *bad = true;
+        len = len < 0 ? 0 : cap;
+    }
+    r.len = len;
+    return r;
+}
+
+// Positions some token of row (len, n) sees: [0, head) and [lo, len), head <= lo.
+__device__ __forceinline__ void visible_span(const AttnParams &p, int len, int first_pos, int *head, int *lo) {
+    *lo = 0;
+    *head = 0;
+    if (p.window > 0) {
+        const int l = first_pos - p.window + 1;
+        if (l > 0) {
+            *lo = l < len ? l : len;
+            *head = p.sinks < *lo ? p.sinks : *lo;
+        }
+    }
+}
+
+// Streaming attention (paged_attn.cu): up to 16 query rows a (row, KV head).
+size_t stream_ws_bytes(int sms, int d);
+cudaError_t stream_configure();
+cudaError_t stream_launch(const AttnParams &p, int sms, cudaStream_t st);
+
+}  // namespace paged
+}  // namespace tiles
