@@ -26,8 +26,7 @@
 
 #include <algorithm>
 
-#include "megakernel.cuh"
-#include "paged_internal.h"
+#include "paged_device.cuh"
 
 namespace tiles {
 namespace paged {
@@ -55,17 +54,6 @@ __device__ __forceinline__ uint2 ld_stream8(const uint8_t *p) {
     asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
     return v;
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t cvt_bf2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // The INT8 codes in bytes 0 and 2 of y (bytes 1 and 3: anything) as a BF16
 // pair, exactly: (0x43, c & 127) - (0x43, c & 128) as BF16 numbers is c.
 __device__ __forceinline__ uint32_t pair_codes(uint32_t y) {
@@ -95,53 +83,6 @@ __device__ __forceinline__ Item item_of(const AttnParams &p, int s, bool *bad) {
     if (it.nhu > it.wu0) it.nhu = it.wu0;
     it.nb = r.n > 0 ? it.nhu + (r.len + UP - 1) / UP - it.wu0 : 0;
     return it;
-}
-
-// Row r of (s, h) again, position by position with nothing but what it sees:
-// for rows whose matrix product met an infinity or NaN in a value row that only
-// other rows of the tile see (0 * inf). One warp; D / 32 dimensions a lane.
-template <int D, bool I8>
-__device__ __noinline__ void row_again(const AttnParams &p, int s, int h, int t0, int n, int len, int r) {
-    constexpr int E = D / 32;
-    const View &c = p.c;
-    const int lane = threadIdx.x & 31, tok = r / p.G, pos = len - n + tok, hq = h * p.G + r % p.G;
-    const uint16_t *q = p.q + (t0 + tok) * p.q_t + hq * p.q_h;
-    float qf[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        qf[e] = bf2f(q[lane * E + e]);
-        o[e] = 0.f;
-    }
-    for (int pass = 0; pass < 2; ++pass)
-        for (int t = 0; t <= pos && t < len; ++t) {
-            if (p.window > 0 && t <= pos - p.window && t >= p.sinks) continue;
-            const int page = c.tables[(size_t)s * c.width + t / c.ps];
-            if (page < 0 || page >= c.n_pages) continue;
-            const size_t at = ((size_t)page * c.nkv + h) * c.ps + t % c.ps;
-            float x = 0.f, v[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const size_t i = at * D + lane * E + e;
-                const float kf = I8 ? (float)reinterpret_cast<const int8_t *>(c.k)[i]
-                                    : bf2f(reinterpret_cast<const uint16_t *>(c.k)[i]);
-                v[e] = I8 ? (float)reinterpret_cast<const int8_t *>(c.v)[i] * c.vs[at]
-                          : bf2f(reinterpret_cast<const uint16_t *>(c.v)[i]);
-                x = fmaf(qf[e], kf, x);
-            }
-            x = warp_sum(x) * p.scale_log2;
-            if (I8) x *= c.ks[at];
-            if (pass == 0) {
-                m = x > m || x != x ? x : m;
-            } else {
-                const float w = exp2f(x - (m == -INFINITY ? 0.f : m));
-                l += w;
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[e], o[e]);
-            }
-        }
-    uint16_t *out = p.out + (t0 + tok) * p.o_t + hq * p.o_h;
-#pragma unroll
-    for (int e = 0; e < E; ++e) out[lane * E + e] = l == 0.f ? 0 : f2bf(o[e] / l);
 }
 
 template <int D, bool I8, int RT>
@@ -279,9 +220,9 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
             // pool row of position tb (a multiple of 16), or -1: outside the length, or no page
             auto pool_row = [&](int tb) -> long long {
                 if (tb >= it.len) return -1;
-                const int page = __ldg(table + tb / c.ps);
+                const int page = __ldg(table + (tb >> c.psl));
                 if (page < 0 || page >= c.n_pages) return -2;
-                return ((long long)page * c.nkv + h) * c.ps + tb % c.ps;
+                return ((long long)page * c.nkv + h) * c.ps + (tb & (c.ps - 1));
             };
             long long krow[NB], nrow[NB];
             auto load_k = [&](const long long (&row)[NB]) {

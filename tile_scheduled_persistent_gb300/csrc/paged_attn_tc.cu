@@ -1,0 +1,857 @@
+// Attention of many query rows per (sequence, KV head) over a paged KV cache:
+// prompts, pieces of prompts, draft tokens, on the fifth-generation tensor
+// cores.
+//
+//   out_r = sum_t softmax_t(scale q_r . K_t) V_t   over the positions t row r sees
+//
+// The query heads of a KV head and the tokens of a sequence are rows of one
+// matrix (row = token * group + head of the group), so a KV head's keys and
+// values are read once for all of them. A CTA works on two tiles of 128 rows
+// (a "pair") and walks the positions in blocks of 128:
+//   - the loader (one warp): each page of a block as boxes of page_size x 64
+//     dimensions into a ring of shared-memory blocks (K, V, K, V ...), 128-byte
+//     swizzle. The values that no row may see (behind the end, missing pages) are
+//     set to zero in shared memory, as 0 * NaN would not vanish. With an INT8
+//     cache the loader is four warps that read the codes, widen them to BF16
+//     (exactly) and store them in the same layout; the scales go beside them.
+//   - the MMA issuer (one lane): S_i = Q_i K^T (128 x 128 in tensor memory), and,
+//     when the softmax has turned S_i into weights in place, O_i += P_i V with P_i
+//     read from tensor memory. While one tile's rows are in the softmax the tensor
+//     cores work on the other tile.
+//   - a softmax warpgroup per tile, one row a thread: running maximum and sum in
+//     FP32, no shuffles. O_i is rescaled only when a row's maximum has risen by
+//     more than 8 powers of two since it was last set (weights stay below 2^8,
+//     which neither BF16 nor the FP32 sums mind), so hardly ever after the first
+//     block.
+// Weights enter P V as BF16 (2^-9 relative each, random in sign): a second product
+// for the remainder would cost half as much again where the tensor cores are the
+// bound, and the output is BF16 itself.
+// The work is cut as in the streaming kernel: the blocks of all pairs form one
+// line, each CTA (one per SM) takes an equal piece, pairs that several CTAs share
+// are joined afterwards. Every wait is bounded; past the limit the CTA records a
+// timeout, lets its copies and MMAs finish (bounded too), frees its tensor memory
+// and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "paged_device.cuh"
+
+namespace tiles {
+namespace paged {
+
+constexpr int kBlock = 128;      // positions a block
+constexpr int kTile = 128;       // query rows a tile
+constexpr int kPair = 2 * kTile; // query rows a CTA works on at a time
+constexpr int kMaxRing = 8;
+constexpr int kMaskRing = 16;
+constexpr unsigned long long kTimeoutNs = 2000000000ull;
+constexpr float kRise = 8.0f;    // powers of two a maximum may rise before O is rescaled
+
+template <int D, bool I8>
+struct TcShape {
+    static constexpr int HALF = kBlock * 128;           // bytes: 128 rows of 64 BF16
+    static constexpr int BLOCK = HALF * (D / 64);       // one block of K or V, or a query tile
+    static constexpr int RING = I8 ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 8);
+    static constexpr int LOADERS = I8 ? 4 : 1;          // warps
+    static constexpr int THREADS = (8 + 1 + LOADERS) * 32;
+    static constexpr int LD = D + 4;                    // floats a row of a partial state
+    static constexpr int SCALES = I8 ? 2 * 16 * kBlock * 4 : 0;  // bytes: a block's K and V scales, by block number
+};
+
+struct Ctl {
+    uint64_t full[kMaxRing], empty[kMaxRing], fix, drain, q_ready[2], s_full[2], p_full[2], o_full[2];
+    uint32_t tmem, abort;
+    uint32_t mask[kMaskRing];    // pages of a key block that are there, by block number
+    int seg_s, seg_h, seg_m;
+    long long seg_at, scan[16];
+};
+
+struct SegRec {
+    int parts, s, h, m, slot, pad[3];
+};
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {  // K-major, 128-byte swizzle, 8-row groups 1024 bytes apart
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+           ((uint64_t)2 << 61);
+}
+// MN-major, 128-byte swizzle: 64 consecutive elements of N a row of 128 bytes,
+// the next 64 a half block further (leading offset), groups of 8 k-rows 1024
+// bytes apart (stride offset)
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lead) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint32_t idesc(int n, bool b_mn) {  // M 128, BF16 x BF16 -> FP32
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+#define R8(a, o) "=r"(a[o]), "=r"(a[o + 1]), "=r"(a[o + 2]), "=r"(a[o + 3]), "=r"(a[o + 4]), "=r"(a[o + 5]), "=r"(a[o + 6]), "=r"(a[o + 7])
+#define V8(a, o) "r"(a[o]), "r"(a[o + 1]), "r"(a[o + 2]), "r"(a[o + 3]), "r"(a[o + 4]), "r"(a[o + 5]), "r"(a[o + 6]), "r"(a[o + 7])
+// 32 consecutive columns of this thread's tensor-memory lane, complete on return
+__device__ __forceinline__ void tld32(uint32_t t, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24)
+        : "r"(t)
+        : "memory");
+}
+__device__ __forceinline__ void tld64(uint32_t t, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, "
+        "%38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, "
+        "%60, %61, %62, %63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24), R8(r, 32), R8(r, 40), R8(r, 48), R8(r, 56)
+        : "r"(t)
+        : "memory");
+}
+__device__ __forceinline__ void tst32(uint32_t t, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(t),
+        V8(r, 0), V8(r, 8), V8(r, 16), V8(r, 24)
+        : "memory");
+}
+__device__ __forceinline__ void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ------------------------------------------------------------------ the line of blocks
+// Pair m of (row, head): query rows 256 m .. of n G, the positions that some
+// row of it sees, as blocks: nhb of [0, head), the rest from block wb0 on.
+struct PairSpan {
+    int rows, p_first, p_last, head, lo, hi, nhb, wb0, nb;
+};
+__device__ __forceinline__ PairSpan pair_span(const AttnParams &p, const RowSpan &r, int m) {
+    PairSpan a;
+    const int r0 = m * kPair;
+    a.rows = min(kPair, r.n * p.G - r0);
+    const int base = r.len - r.n;
+    a.p_first = base + r0 / p.G;
+    a.p_last = base + (r0 + a.rows - 1) / p.G;
+    a.hi = max(0, a.p_last + 1);
+    visible_span(p, a.hi, a.p_first, &a.head, &a.lo);
+    a.nhb = (a.head + kBlock - 1) / kBlock;
+    a.wb0 = a.lo / kBlock;
+    if (a.nhb > a.wb0) a.nhb = a.wb0;
+    a.nb = a.rows > 0 ? a.nhb + (a.hi + kBlock - 1) / kBlock - a.wb0 : 0;
+    return a;
+}
+__device__ __forceinline__ int pairs_of(const AttnParams &p, const RowSpan &r) { return (r.n * p.G + kPair - 1) / kPair; }
+
+// Blocks of one head of each of 32 rows (one a lane): rows of several pairs are
+// added up by the whole warp.
+__device__ __forceinline__ int row_blocks(const AttnParams &p, const RowSpan &r, int lane) {
+    const int np = pairs_of(p, r);
+    int nb = np == 1 ? pair_span(p, r, 0).nb : 0;
+    uint32_t many = __ballot_sync(0xFFFFFFFFu, np > 1);
+    while (many) {
+        const int src = __ffs(many) - 1;
+        many &= many - 1;
+        RowSpan q;
+        q.t0 = 0;
+        q.n = __shfl_sync(0xFFFFFFFFu, r.n, src);
+        q.len = __shfl_sync(0xFFFFFFFFu, r.len, src);
+        const int k = pairs_of(p, q);
+        int sum = 0;
+        for (int m = lane; m < k; m += 32) sum += pair_span(p, q, m).nb;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (lane == src) nb = sum;
+    }
+    return nb;
+}
+
+// A walk over the pairs from (s, h, m) on; every role of the CTA walks alike.
+struct Walk {
+    int s, h, m;
+    RowSpan r;
+    PairSpan a;
+    __device__ __forceinline__ void load(const AttnParams &p) {
+        bool bad = false;
+        r = row_span(p, s, &bad);
+        a = pair_span(p, r, m);
+    }
+    // the next pair with blocks; only called where more blocks follow
+    __device__ __forceinline__ void next(const AttnParams &p) {
+        do {
+            if (++m >= pairs_of(p, r)) {
+                m = 0;
+                if (++h >= p.c.nkv || r.n == 0) {
+                    h = 0;
+                    if (++s >= p.c.n_seqs) {
+                        s = p.c.n_seqs - 1;
+                        a.nb = 0;
+                        return;
+                    }
+                    bool bad = false;
+                    r = row_span(p, s, &bad);
+                }
+            }
+            a = pair_span(p, r, m);
+        } while (a.nb == 0);
+    }
+};
+
+__device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity, unsigned long long deadline,
+                                             volatile uint32_t *abort) {
+    for (uint32_t spin = 0;; ++spin) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((spin & 63u) == 63u && (*abort || global_timer() > deadline)) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the kernel
+template <int D, bool I8>
+__global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
+    tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ TensorMap mk, const __grid_constant__ TensorMap mv) {
+    using S = TcShape<D, I8>;
+    constexpr int RING = S::RING, LD = S::LD, NW = S::THREADS / 32;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint8_t *sq = sm;                     // two query tiles
+    uint8_t *ring = sm + 2 * S::BLOCK;    // RING blocks
+    Ctl *ctl = reinterpret_cast<Ctl *>(ring + RING * S::BLOCK + S::SCALES);
+    float(*scale)[kMaskRing][kBlock] = reinterpret_cast<float(*)[kMaskRing][kBlock]>(ring + RING * S::BLOCK);  // INT8
+    const View &c = p.c;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+    SegRec *recs = reinterpret_cast<SegRec *>(p.ws);
+    float *parts = p.ws + (size_t)p.ctas * (sizeof(SegRec) / 4);
+    if (smem_u32(sm) & 1023u) {  // the swizzle counts on it
+        if (tid == 0) {
+            recs[cta].parts = 0;
+            atomicOr(reinterpret_cast<uint32_t *>(c.state), kDevBounds);
+        }
+        return;
+    }
+    if (tid == 0) {
+        recs[cta].parts = 0;
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(&ctl->full[i], I8 ? 128 : 1);
+            mbar_init(&ctl->empty[i], 1);
+        }
+        mbar_init(&ctl->fix, 1);
+        mbar_init(&ctl->drain, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->q_ready[i], 128);
+            mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->p_full[i], 128);
+            mbar_init(&ctl->o_full[i], 1);
+        }
+        ctl->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // ---- this CTA's piece of the line: warp w sums rows [w per, (w + 1) per)
+    const int per = (c.n_seqs + NW - 1) / NW, sa = warp * per, sb = min(c.n_seqs, sa + per);
+    long long mine = 0;
+    for (int s0 = sa; s0 < sb; s0 += 32) {
+        RowSpan r = {0, 0, 0};
+        bool bad = false;
+        if (s0 + lane < sb) r = row_span(p, s0 + lane, &bad);
+        mine += row_blocks(p, r, lane);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+    mine *= c.nkv;
+    if (lane == 0) ctl->scan[warp] = mine;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < NW; ++w) {
+        if (w < warp) before += ctl->scan[w];
+        total += ctl->scan[w];
+    }
+    const long long nc = min((long long)p.ctas, total);
+    const long long begin = cta < nc ? cta * total / nc : 0, end = cta < nc ? (cta + 1) * total / nc : 0;
+    if (begin < end && begin >= before && begin < before + mine) {
+        // the row, then the head, then the pair that holds block `begin`
+        long long at = before;
+        bool hit = false;
+        for (int s0 = sa; s0 < sb && !hit; s0 += 32) {
+            RowSpan r = {0, 0, 0};
+            bool bad = false;
+            if (s0 + lane < sb) r = row_span(p, s0 + lane, &bad);
+            const int nb = row_blocks(p, r, lane);
+            long long x = (long long)nb * c.nkv;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+                if (lane >= o) x += y;
+            }
+            const uint32_t in = __ballot_sync(0xFFFFFFFFu, begin < at + x);
+            if (in) {
+                const int src = __ffs(in) - 1;
+                const int row_nb = __shfl_sync(0xFFFFFFFFu, nb, src);
+                const long long row_at = at + __shfl_sync(0xFFFFFFFFu, x, src) - (long long)row_nb * c.nkv;
+                RowSpan q;
+                q.t0 = 0;
+                q.n = __shfl_sync(0xFFFFFFFFu, r.n, src);
+                q.len = __shfl_sync(0xFFFFFFFFu, r.len, src);
+                const int h = (int)((begin - row_at) / row_nb);
+                long long pos = row_at + (long long)h * row_nb;
+                const int np = pairs_of(p, q);
+                for (int m0 = 0; m0 < np; m0 += 32) {
+                    int k = m0 + lane < np ? pair_span(p, q, m0 + lane).nb : 0, y = k;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int z = __shfl_up_sync(0xFFFFFFFFu, y, o);
+                        if (lane >= o) y += z;
+                    }
+                    const uint32_t got = __ballot_sync(0xFFFFFFFFu, begin < pos + y);
+                    if (got) {
+                        if (lane == __ffs(got) - 1) {
+                            ctl->seg_s = s0 + src;
+                            ctl->seg_h = h;
+                            ctl->seg_m = m0 + lane;
+                            ctl->seg_at = pos + y - k;
+                        }
+                        break;
+                    }
+                    pos += __shfl_sync(0xFFFFFFFFu, y, 31);
+                }
+                hit = true;
+            }
+            at += __shfl_sync(0xFFFFFFFFu, x, 31);
+        }
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl->tmem)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = ctl->tmem;
+    volatile uint32_t *abort = &ctl->abort;
+    const unsigned long long deadline = global_timer() + kTimeoutNs;
+    bool ok = true;
+    // MMAs and copies this thread has issued, for the way out
+    int issued = 0;
+
+    if (begin < end) {
+        Walk w;
+        w.s = ctl->seg_s;
+        w.h = ctl->seg_h;
+        w.m = ctl->seg_m;
+        w.load(p);
+        long long at = ctl->seg_at, pos = begin;
+        auto block_of = [&](int b) { return b < w.a.nhb ? b : b - w.a.nhb + w.a.wb0; };
+
+        if (warp >= 9) {
+            // ================================================ loader
+            const int lt = tid - 9 * 32;  // thread of the loader
+            int n = 0;                    // blocks of K and V so far
+            uint32_t kb = 0, fixes = 0;   // key blocks, repaired blocks so far
+            while (pos < end && ok) {
+                const int b0 = (int)(pos - at), b1 = (int)min((long long)w.a.nb, end - at);
+                const int32_t *table = c.tables + (size_t)w.s * c.width;
+                for (int b = b0; b < b1 && ok; ++b) {
+                    const int t0 = block_of(b) * kBlock, npg = kBlock / c.ps;
+                    // lane i: page i of the block, -1 where nothing of it is seen, or it is missing
+                    int page = -1;
+                    bool wanted = false;
+                    if (lane < npg) {
+                        const int pa = t0 + lane * c.ps, pe = pa + c.ps;
+                        wanted = pa < w.a.hi && (pe > w.a.lo || pa < w.a.head);
+                        if (wanted) {
+                            page = __ldg(table + (pa >> c.psl));
+                            if (page < 0 || page >= c.n_pages) {
+                                page = -1;
+                                atomicOr(reinterpret_cast<uint32_t *>(c.state), kDevBounds);
+                            }
+                        }
+                    }
+                    const uint32_t have = __ballot_sync(0xFFFFFFFFu, page >= 0);
+                    // bits of 16 positions, for the softmax
+                    uint32_t mask16 = 0;
+                    for (int i = 0; i < 8; ++i) mask16 |= ((have >> ((16 * i) >> c.psl)) & 1u) << i;
+                    for (int kv = 0; kv < 2 && ok; ++kv, ++n) {
+                        const int st = n % RING, round = n / RING;
+                        if (round > 0)
+                            ok = __all_sync(0xFFFFFFFFu, bounded_wait(&ctl->empty[st], (uint32_t)(round - 1) & 1u, deadline, abort));
+                        if (!ok) break;
+                        uint8_t *dst = ring + st * S::BLOCK;
+                        if (kv == 0 && lt == 0) ctl->mask[kb % kMaskRing] = mask16;
+                        if constexpr (!I8) {
+                            // rows of V that nothing may read: zero them once the copies are in
+                            const bool repair = kv == 1 && (have != (1u << npg) - 1u ||
+                                                            t0 + kBlock > w.a.hi);
+                            uint64_t *bar = repair ? &ctl->fix : &ctl->full[st];
+                            if (lane == 0) mbar_expect_tx(bar, (uint32_t)(__popc(have) * c.ps * D * 2));
+                            __syncwarp();
+                            if (page >= 0) {
+                                const int z = page * c.nkv + w.h;
+#pragma unroll
+                                for (int hf = 0; hf < D / 64; ++hf)
+                                    tensor_g2s_3d(dst + hf * S::HALF + lane * c.ps * 128, kv ? &mv : &mk, 64 * hf, 0, z, bar);
+                            }
+                            if (repair) {
+                                ok = __all_sync(0xFFFFFFFFu, bounded_wait(&ctl->fix, fixes & 1u, deadline, abort));
+                                if (!ok) break;
+                                ++fixes;
+                                for (int i = lane; i < kBlock * (D / 8); i += 32) {
+                                    const int row = i / (D / 8), u = i % (D / 8);
+                                    if (!((mask16 >> (row / 16)) & 1u) || t0 + row >= w.a.hi)
+                                        *reinterpret_cast<uint4 *>(dst + (u / 8) * S::HALF + row * 128 + (((u % 8) ^ (row & 7)) << 4)) =
+                                            make_uint4(0u, 0u, 0u, 0u);
+                                }
+                                fence_proxy_async_smem();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&ctl->full[st]);
+                            }
+                        } else {
+                            // 16 codes a step: a row is D / 16 steps
+                            const uint8_t *pool = kv ? c.v : c.k;
+                            const float *scales = kv ? c.vs : c.ks;
+                            constexpr int UPR = D / 16, STEPS = kBlock * UPR / 128;
+                            uint4 w4[STEPS];
+#pragma unroll
+                            for (int k = 0; k < STEPS; ++k) {
+                                const int i = lt + 128 * k, row = i / UPR, u = i % UPR;
+                                const int pg = __shfl_sync(0xFFFFFFFFu, page, row >> c.psl);
+                                w4[k] = make_uint4(0u, 0u, 0u, 0u);
+                                if (pg >= 0 && (kv == 0 || t0 + row < w.a.hi))
+                                    w4[k] = __ldg(reinterpret_cast<const uint4 *>(
+                                        pool + (((size_t)pg * c.nkv + w.h) * c.ps + (row & (c.ps - 1))) * D + 16 * u));
+                            }
+                            const int pg = __shfl_sync(0xFFFFFFFFu, page, lt >> c.psl);  // of this thread's row
+                            float f = 0.f;
+                            if (pg >= 0 && t0 + lt < w.a.hi)
+                                f = __ldg(scales + ((size_t)pg * c.nkv + w.h) * c.ps + (lt & (c.ps - 1)));
+                            scale[kv][kb % kMaskRing][lt] = f;
+#pragma unroll
+                            for (int k = 0; k < STEPS; ++k) {
+                                const int i = lt + 128 * k, row = i / UPR, u = i % UPR;
+                                const uint32_t x[4] = {w4[k].x, w4[k].y, w4[k].z, w4[k].w};
+                                uint32_t y[8];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) codes_bf16x2(x[j], y[2 * j], y[2 * j + 1]);
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const int uu = 2 * u + j;
+                                    *reinterpret_cast<uint4 *>(dst + (uu / 8) * S::HALF + row * 128 + (((uu % 8) ^ (row & 7)) << 4)) =
+                                        make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                                }
+                            }
+                            fence_proxy_async_smem();
+                            mbar_arrive(&ctl->full[st]);
+                        }
+                    }
+                    ++kb;
+                }
+                pos = at + b1;
+                if (pos < end) {
+                    at += w.a.nb;
+                    w.next(p);
+                }
+            }
+            issued = n;
+        } else if (warp == 8) {
+            // ================================================ MMA issuer
+            if (lane == 0) {
+                const uint32_t id_s = idesc(kBlock, false), id_o = idesc(D, true);
+                const uint32_t o_tm = tmem + 256;
+                int n = 0;
+                uint32_t seg[2] = {0, 0}, step[2] = {0, 0};
+                auto s_mma = [&](int i, int st) {
+                    const uint64_t a = desc_k(smem_u32(sq + i * S::BLOCK)), b = desc_k(smem_u32(ring + st * S::BLOCK));
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t off = (uint64_t)((k / 4) * (S::HALF >> 4) + (k % 4) * 2);
+                        mma_ss(tmem + 128 * i, a + off, b + off, id_s, k != 0);
+                    }
+                    commit(&ctl->s_full[i]);
+                };
+                while (pos < end && ok) {
+                    const int b0 = (int)(pos - at), b1 = (int)min((long long)w.a.nb, end - at);
+                    const int nt = w.a.rows > kTile ? 2 : 1;
+                    ok = bounded_wait(&ctl->full[n % RING], (uint32_t)(n / RING) & 1u, deadline, abort);
+                    for (int i = 0; i < nt && ok; ++i) {
+                        ok = bounded_wait(&ctl->q_ready[i], seg[i] & 1u, deadline, abort);
+                        if (!ok) break;
+                        ++seg[i];
+                        fence_after();
+                        issued = 1;
+                        s_mma(i, n % RING);
+                    }
+                    if (!ok) break;
+                    commit(&ctl->empty[n % RING]);
+                    for (int b = b0; b < b1 && ok; ++b, n += 2) {
+                        const int sv = (n + 1) % RING, sk = (n + 2) % RING;
+                        ok = bounded_wait(&ctl->full[sv], (uint32_t)((n + 1) / RING) & 1u, deadline, abort);
+                        if (!ok) break;
+                        for (int i = 0; i < nt && ok; ++i) {
+                            ok = bounded_wait(&ctl->p_full[i], step[i] & 1u, deadline, abort);
+                            if (!ok) break;
+                            ++step[i];
+                            fence_after();
+                            const uint64_t bv = desc_mn(smem_u32(ring + sv * S::BLOCK), S::HALF);
+#pragma unroll
+                            for (int k = 0; k < kBlock / 16; ++k)
+                                mma_ts(o_tm + D * i, tmem + 128 * i + 8 * k, bv + (uint64_t)(k * (2048 >> 4)), id_o,
+                                       b > b0 || k > 0);
+                            if (i == nt - 1) commit(&ctl->empty[sv]);
+                            if (b + 1 < b1) {
+                                if (i == 0) {
+                                    ok = bounded_wait(&ctl->full[sk], (uint32_t)((n + 2) / RING) & 1u, deadline, abort);
+                                    if (!ok) break;
+                                    fence_after();
+                                }
+                                s_mma(i, sk);
+                                if (i == nt - 1) commit(&ctl->empty[sk]);
+                            } else {
+                                commit(&ctl->o_full[i]);
+                            }
+                        }
+                    }
+                    pos = at + b1;
+                    if (pos < end) {
+                        at += w.a.nb;
+                        w.next(p);
+                    }
+                }
+            }
+            __syncwarp();
+        } else {
+            // ================================================ softmax, one query row a thread
+            const int i = warp >> 2, row = tid & 127;
+            const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+            const uint32_t s_tm = tmem + 128 * i + lanes, o_tm = tmem + 256 + D * i + lanes;
+            uint32_t step = 0, seg = 0, kb = 0;
+            uint32_t n = 0;  // ring blocks before the current key block
+            while (pos < end && ok) {
+                const int b0 = (int)(pos - at), b1 = (int)min((long long)w.a.nb, end - at);
+                const int r = w.m * kPair + i * kTile + row;     // of the (sequence, KV head)
+                const bool mine_row = i * kTile + row < w.a.rows;
+                const bool tile_on = i * kTile < w.a.rows;
+                const int tok = r / p.G, hq = w.h * p.G + r % p.G;
+                const int lim = mine_row ? w.r.len - w.r.n + tok : -1;
+                if (tile_on) {
+                    const uint16_t *q = p.q + (w.r.t0 + tok) * p.q_t + (long long)hq * p.q_h;
+                    uint8_t *dst = sq + i * S::BLOCK + row * 128;
+#pragma unroll
+                    for (int u = 0; u < D / 8; ++u) {
+                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                        if (mine_row) x = __ldg(reinterpret_cast<const uint4 *>(q + 8 * u));
+                        *reinterpret_cast<uint4 *>(dst + (u / 8) * S::HALF + (((u % 8) ^ (row & 7)) << 4)) = x;
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(&ctl->q_ready[i]);
+                }
+                float mx = -INFINITY, l = 0.f;
+                if (tile_on) {
+                    // positions every row of the tile sees
+                    const int ra = w.m * kPair + i * kTile, rz = min(ra + kTile, w.m * kPair + w.a.rows) - 1;
+                    const int all_hi = w.r.len - w.r.n + ra / p.G;
+                    const int all_lo = p.window > 0 ? w.r.len - w.r.n + rz / p.G - p.window + 1 : 0;
+                    for (int b = b0; b < b1; ++b, ++kb, n += 2) {
+                        ok = bounded_wait(&ctl->s_full[i], step & 1u, deadline, abort);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                        ++step;
+                        fence_after();
+                        const int t0 = block_of(b) * kBlock;
+                        const uint32_t mask = ctl->mask[kb % kMaskRing];
+                        uint32_t s0[64], s1[64];
+                        tld64(s_tm, s0);
+                        tld64(s_tm + 64, s1);
+                        auto x = [&](int j) -> uint32_t & { return j < 64 ? s0[j] : s1[j - 64]; };
+                        if constexpr (I8) {
+                            const float *ks = scale[0][kb % kMaskRing];
+#pragma unroll
+                            for (int j = 0; j < kBlock; ++j) x(j) = __float_as_uint(__uint_as_float(x(j)) * ks[j]);
+                        }
+                        if (mask != 0xFFu || t0 + kBlock - 1 > all_hi || t0 < all_lo) {
+#pragma unroll
+                            for (int j = 0; j < kBlock; ++j) {
+                                const int t = t0 + j;
+                                const bool see = t <= lim && (p.window == 0 || t > lim - p.window || t < p.sinks) &&
+                                                 ((mask >> (j / 16)) & 1u);
+                                if (!see) x(j) = 0xFF800000u;
+                            }
+                        }
+                        float bm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int j = 0; j < kBlock; j += 8)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                bm[k] = fmaxf(bm[k], fmaxf(__uint_as_float(x(j + k)), __uint_as_float(x(j + 4 + k))));
+                        const float top = fmaxf(fmaxf(bm[0], bm[1]), fmaxf(bm[2], bm[3])) * p.scale_log2;
+                        const bool rise = top > mx + kRise || (mx == -INFINITY && top > mx);
+                        if (__any_sync(0xFFFFFFFFu, rise)) {
+                            const float nm = rise ? top : mx;
+                            const float corr = nm > mx ? ex2(mx - nm) : 1.f;
+                            mx = nm;
+                            l *= corr;
+                            if (b > b0) {
+                                // the last P V is complete: it was issued before this block's S
+                                for (int d = 0; d < D; d += 32) {
+                                    uint32_t o[32];
+                                    tld32(o_tm + d, o);
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+                                    tst32(o_tm + d, o);
+                                }
+                            }
+                        }
+                        const float base = mx == -INFINITY ? 0.f : mx;
+                        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                        const float *vs = nullptr;
+                        if constexpr (I8) {
+                            // the value block's scales: its copy is in once the block after the keys is full
+                            ok = bounded_wait(&ctl->full[(n + 1) % RING], ((n + 1) / RING) & 1u, deadline, abort);
+                            ok = __all_sync(0xFFFFFFFFu, ok);
+                            if (!ok) break;
+                            vs = scale[1][kb % kMaskRing];
+                        }
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            uint32_t pk[32];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const int k = hf * 64 + 2 * j;
+                                float e0 = ex2(fmaf(__uint_as_float(x(k)), p.scale_log2, -base));
+                                float e1 = ex2(fmaf(__uint_as_float(x(k + 1)), p.scale_log2, -base));
+                                ls[(2 * j) & 3] += e0;
+                                ls[(2 * j + 1) & 3] += e1;
+                                if constexpr (I8) {
+                                    e0 *= vs[k];
+                                    e1 *= vs[k + 1];
+                                }
+                                pk[j] = cvt_bf2(e0, e1);
+                            }
+                            tst32(s_tm + 32 * hf, pk);
+                        }
+                        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                        tst_wait();
+                        fence_before();
+                        mbar_arrive(&ctl->p_full[i]);
+                    }
+                    // ---- the pair's output, or this piece's state
+                    ok = ok && bounded_wait(&ctl->o_full[i], seg & 1u, deadline, abort);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    ++seg;
+                    fence_after();
+                    const bool whole = b0 == 0 && b1 == w.a.nb;
+                    const int slot = pos == begin ? 0 : 1;
+                    if (whole) {
+                        const float inv = l == 0.f ? 0.f : 1.f / l;
+                        bool finite = true;
+                        uint16_t *out = p.out + (w.r.t0 + tok) * p.o_t + (long long)hq * p.o_h;
+                        for (int d = 0; d < D; d += 32) {
+                            uint32_t o[32];
+                            tld32(o_tm + d, o);
+                            float sum = 0.f;
+#pragma unroll
+                            for (int k = 0; k < 32; k += 8) {
+                                float v[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    v[e] = __uint_as_float(o[k + e]) * inv;
+                                    sum += fabsf(v[e]);
+                                }
+                                if (mine_row)
+                                    *reinterpret_cast<uint4 *>(out + d + k) =
+                                        make_uint4(cvt_bf2(v[0], v[1]), cvt_bf2(v[2], v[3]), cvt_bf2(v[4], v[5]), cvt_bf2(v[6], v[7]));
+                            }
+                            finite &= sum < INFINITY;
+                        }
+                        fence_before();
+                        __syncwarp();
+                        uint32_t again = __ballot_sync(0xFFFFFFFFu, mine_row && !finite && w.r.n > 1);
+                        while (again) {
+                            const int src = __ffs(again) - 1;
+                            again &= again - 1;
+                            row_again<D, I8>(p, w.s, w.h, w.r.t0, w.r.n, w.r.len, __shfl_sync(0xFFFFFFFFu, r, src));
+                        }
+                    } else {
+                        float *dst = parts + ((size_t)(2 * cta + slot) * kPair + i * kTile + row) * LD;
+                        for (int d = 0; d < D; d += 32) {
+                            uint32_t o[32];
+                            tld32(o_tm + d, o);
+                            if (mine_row)
+#pragma unroll
+                                for (int k = 0; k < 32; k += 4)
+                                    *reinterpret_cast<uint4 *>(dst + d + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        }
+                        fence_before();
+                        if (mine_row) *reinterpret_cast<float2 *>(dst + D) = make_float2(mx, l);
+                        if (b0 == 0 && tid == 0) {
+                            SegRec rec;
+                            rec.parts = (int)(((at + w.a.nb) * nc + total - 1) / total - 1 - cta) + 1;
+                            rec.s = w.s;
+                            rec.h = w.h;
+                            rec.m = w.m;
+                            rec.slot = slot;
+                            rec.pad[0] = rec.pad[1] = rec.pad[2] = 0;
+                            recs[cta] = rec;
+                        }
+                    }
+                } else {
+                    kb += (uint32_t)(b1 - b0);
+                    n += 2u * (uint32_t)(b1 - b0);
+                }
+                pos = at + b1;
+                if (pos < end) {
+                    at += w.a.nb;
+                    w.next(p);
+                }
+            }
+        }
+    }
+    // ---- pairs that see nothing, rows that break the rules
+    for (int s = cta; s < c.n_seqs; s += gridDim.x) {
+        bool bad = false;
+        const RowSpan r = row_span(p, s, &bad);
+        if (bad && tid == 0) atomicOr(reinterpret_cast<uint32_t *>(c.state), kDevBounds);
+        for (int m = 0; m < pairs_of(p, r); ++m) {
+            const PairSpan a = pair_span(p, r, m);
+            if (a.nb) break;  // later tokens see more
+            for (int i = tid; i < a.rows * c.nkv * (D / 8); i += S::THREADS) {
+                const int u = i % (D / 8), x = i / (D / 8), h = x % c.nkv, q = m * kPair + x / c.nkv;
+                *reinterpret_cast<uint4 *>(p.out + (r.t0 + q / p.G) * p.o_t + (long long)(h * p.G + q % p.G) * p.o_h + 8 * u) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    }
+    // ---- the way out: after a timeout, what is in flight ends first
+    if (!ok) {
+        if (lane == 0) atomicOr(reinterpret_cast<uint32_t *>(c.state), kDevTimeout);
+        const unsigned long long d2 = global_timer() + kTimeoutNs;
+        uint32_t never = 0;
+        if (warp == 8 && lane == 0 && issued) {
+            commit(&ctl->drain);
+            bounded_wait(&ctl->drain, 0u, d2, &never);
+        }
+        if (!I8 && warp == 9 && lane == 0)
+            for (int k = max(0, issued - RING); k < issued; ++k)
+                bounded_wait(&ctl->full[k % RING], (uint32_t)(k / RING) & 1u, d2, &never);
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
+}
+
+// Adds up the states of the pair that CTA blockIdx.x began; a warp per query row.
+template <int D, bool I8>
+__global__ void __launch_bounds__(256) tc_join_kernel(const __grid_constant__ AttnParams p) {
+    using S = TcShape<D, I8>;
+    constexpr int LD = S::LD, E = D / 32;
+    const int lane = threadIdx.x & 31, cta = blockIdx.x, q = blockIdx.y * 8 + (threadIdx.x >> 5);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const SegRec rec = reinterpret_cast<const SegRec *>(p.ws)[cta];
+    if (rec.parts == 0) return;
+    bool bad = false;
+    const RowSpan r = row_span(p, rec.s, &bad);
+    const int row = rec.m * kPair + q;
+    if (row >= r.n * p.G) return;
+    const float *parts = p.ws + (size_t)p.ctas * (sizeof(SegRec) / 4) + (size_t)q * LD;
+    auto part = [&](int i) { return parts + (size_t)(2 * (cta + i) + (i == 0 ? rec.slot : 0)) * kPair * LD; };
+    float M = -INFINITY;
+    for (int i = lane; i < rec.parts; i += 32) M = fmaxf(M, __ldcg(part(i) + D));
+    M = warp_max(M);
+    const float base = M == -INFINITY ? 0.f : M;
+    float o[E], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < rec.parts; ++i) {
+        const float *a = part(i);
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a + D));
+        const float f = ex2(ml.x - base);
+        l = fmaf(f, ml.y, l);
+        float v[E];
+        if constexpr (E == 4)
+            *reinterpret_cast<float4 *>(v) = __ldcg(reinterpret_cast<const float4 *>(a + 4 * lane));
+        else
+            *reinterpret_cast<float2 *>(v) = __ldcg(reinterpret_cast<const float2 *>(a + 2 * lane));
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(f, v[e], o[e]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t *out = p.out + (r.t0 + row / p.G) * p.o_t + (long long)(rec.h * p.G + row % p.G) * p.o_h + E * lane;
+    float sum = l;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        *reinterpret_cast<uint32_t *>(out + e) = cvt_bf2(o[e] * inv, o[e + 1] * inv);
+        sum += fabsf(o[e]) + fabsf(o[e + 1]);
+    }
+    __syncwarp();
+    if (r.n > 1 && __any_sync(0xFFFFFFFFu, !(sum < INFINITY))) row_again<D, I8>(p, rec.s, rec.h, r.t0, r.n, r.len, row);
+}
+
+// ------------------------------------------------------------------ host side
+size_t tc_ws_bytes(int sms, int d) { return (size_t)sms * (sizeof(SegRec) + (size_t)2 * kPair * (d + 4) * 4); }
+
+template <int D, bool I8>
+static cudaError_t launch(const AttnParams &p, cudaStream_t st) {
+    using S = TcShape<D, I8>;
+    constexpr int smem = (2 + S::RING) * S::BLOCK + S::SCALES + (int)sizeof(Ctl);
+    static_assert(smem > 116 * 1024 && smem <= kSmemLimit, "one CTA per SM, so that none waits for tensor memory");
+    TensorMap mk, mv;
+    if constexpr (I8) {
+        std::memset(&mk, 0, sizeof mk);
+        mv = mk;
+    } else {
+        const uint64_t blocks = (uint64_t)p.c.n_pages * p.c.nkv;
+        if (!encode_bf16_3d(&mk, p.c.k, D, (uint64_t)p.c.ps, blocks, (uint32_t)p.c.ps) ||
+            !encode_bf16_3d(&mv, p.c.v, D, (uint64_t)p.c.ps, blocks, (uint32_t)p.c.ps))
+            return cudaErrorInvalidValue;
+    }
+    cudaError_t e = cudaFuncSetAttribute(tc_kernel<D, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    tc_kernel<D, I8><<<p.ctas, S::THREADS, smem, st>>>(p, mk, mv);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)p.ctas, kPair / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tc_join_kernel<D, I8>, p);
+}
+
+cudaError_t tc_launch(const AttnParams &p0, int sms, cudaStream_t st) {
+    AttnParams p = p0;
+    p.ctas = sms;
+    if (p.c.d == 64) return p.c.i8 ? launch<64, true>(p, st) : launch<64, false>(p, st);
+    return p.c.i8 ? launch<128, true>(p, st) : launch<128, false>(p, st);
+}
+
+}  // namespace paged
+}  // namespace tiles

@@ -537,6 +537,7 @@ View view_of(const tiles_paged_cache &c, int layer) {
     v.nkv = d.n_kv_heads;
     v.d = d.head_dim;
     v.ps = d.page_size;
+    v.psl = d.page_size == 16 ? 4 : d.page_size == 32 ? 5 : d.page_size == 64 ? 6 : 7;
     v.n_pages = d.n_pages;
     v.n_seqs = d.n_seqs;
     v.width = d.table_width;
@@ -550,6 +551,15 @@ tiles_status_t sm_count(int *sms) {
         cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return TILES_ERR_CUDA;
     return TILES_OK;
+}
+
+// Up to 16 query rows a (sequence, KV head) fit one MMA tile of the streaming
+// kernel, which is bound by the cache's bytes; more go to the tensor cores.
+bool streams(int G, int max_tokens) { return (long long)G * max_tokens <= 16; }
+
+int64_t attn_ws_bytes(const tiles_paged_desc &d, int n_q_heads, int max_tokens, int sms) {
+    return (int64_t)(streams(n_q_heads / d.n_kv_heads, max_tokens) ? stream_ws_bytes(sms, d.head_dim)
+                                                                  : tc_ws_bytes(sms, d.head_dim));
 }
 
 tiles_status_t launched() { return cudaGetLastError() == cudaSuccess ? TILES_OK : TILES_ERR_CUDA; }
@@ -662,7 +672,7 @@ tiles_status_t tiles_paged_workspace_bytes(const tiles_paged_desc *desc, int32_t
     if (n_q_heads / desc->n_kv_heads > 16) return TILES_ERR_UNSUPPORTED;
     int sms = 0;
     if ((st = sm_count(&sms)) != TILES_OK) return st;
-    *bytes = (int64_t)stream_ws_bytes(sms, desc->head_dim);
+    *bytes = attn_ws_bytes(*desc, n_q_heads, max_tokens, sms);
     return TILES_OK;
 }
 
@@ -686,7 +696,7 @@ tiles_status_t tiles_paged_attention(const tiles_paged_cache *cache, int32_t lay
     if (max_tokens > n_tokens) max_tokens = n_tokens;
     int sms = 0;
     if ((st = sm_count(&sms)) != TILES_OK) return st;
-    if (workspace_bytes < (int64_t)stream_ws_bytes(sms, d.head_dim)) return TILES_ERR_CAPACITY;
+    if (workspace_bytes < attn_ws_bytes(d, n_q_heads, max_tokens, sms)) return TILES_ERR_CAPACITY;
     AttnParams p;
     p.c = view_of(*cache, layer);
     p.q = static_cast<const uint16_t *>(q);
@@ -704,7 +714,9 @@ tiles_status_t tiles_paged_attention(const tiles_paged_cache *cache, int32_t lay
     p.sinks = window > 0 ? sinks : 0;
     p.ws = static_cast<float *>(workspace);
     p.ctas = 0;
-    return stream_launch(p, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? TILES_OK : TILES_ERR_CUDA;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = streams(p.G, max_tokens) ? stream_launch(p, sms, cs) : tc_launch(p, sms, cs);
+    return e == cudaSuccess ? TILES_OK : TILES_ERR_CUDA;
 }
 
 tiles_status_t tiles_paged_status(const tiles_paged_cache *cache, void *stream) {

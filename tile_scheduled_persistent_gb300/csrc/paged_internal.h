@@ -8,6 +8,11 @@
 #include "tiles_internal.h"
 
 namespace tiles {
+// A 3-D BF16 tensor map (runtime.cu): `blocks` dense blocks of `rows` rows of d
+// elements, boxes of box_rows rows x 64 elements, 128-byte swizzle. False if
+// the driver refuses it.
+bool encode_bf16_3d(TensorMap *out, const void *base, uint64_t d, uint64_t rows, uint64_t blocks, uint32_t box_rows);
+
 namespace paged {
 
 // int32 words of the state buffer: the status word, then (at kStateRefs) the
@@ -25,7 +30,7 @@ struct View {
     float *ks, *vs;      // INT8: scales, likewise
     int32_t *tables, *lens, *state;
     const float *k_shift;  // of the call's layer, or null
-    int n_layers, nkv, d, ps, n_pages, n_seqs, width, i8;
+    int n_layers, nkv, d, ps, psl, n_pages, n_seqs, width, i8;  // psl: log2 of the page size ps
 };
 
 struct AttnParams {
@@ -86,8 +91,11 @@ __device__ __forceinline__ void visible_span(const AttnParams &p, int len, int f
 
 // Streaming attention (paged_attn.cu): up to 16 query rows a (row, KV head).
 size_t stream_ws_bytes(int sms, int d);
-cudaError_t stream_configure();
 cudaError_t stream_launch(const AttnParams &p, int sms, cudaStream_t st);
+
+// Attention on the tensor cores (paged_attn_tc.cu): any number of query rows.
+size_t tc_ws_bytes(int sms, int d);
+cudaError_t tc_launch(const AttnParams &p, int sms, cudaStream_t st);
 
 }  // namespace paged
 }  // namespace tiles

@@ -640,6 +640,21 @@ bool encode_bf16_2d(TensorMap *out, const void *base, uint64_t inner, uint64_t r
     std::memcpy(out, &m, sizeof m);
     return true;
 }
+
+bool encode_bf16_3d(TensorMap *out, const void *base, uint64_t d, uint64_t rows, uint64_t blocks, uint32_t box_rows) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)blocks};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)(d * rows * 2)};
+    const cuuint32_t box[3] = {64, box_rows, 1}, ones[3] = {1, 1, 1};
+    CUtensorMap m;
+    if (enc(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    std::memcpy(out, &m, sizeof m);
+    return true;
+}
 }  // namespace tiles
 
 // ---------------------------------------------------------------------------
