@@ -14,7 +14,7 @@
 //     set to zero in shared memory, as 0 * NaN would not vanish. With an INT8
 //     cache the loader is four warps that read the codes, widen them to BF16
 //     (exactly) and store them in the same layout; the scales go beside them.
-//   - the MMA issuer (one lane): S_i = Q_i K^T (128 x 128 in tensor memory), and,
+//   - the MMA issuer (one warp): S_i = Q_i K^T (128 x 128 in tensor memory), and,
 //     when the softmax has turned S_i into weights in place, O_i += P_i V with P_i
 //     read from tensor memory. While one tile's rows are in the softmax the tensor
 //     cores work on the other tile.
@@ -56,14 +56,16 @@ struct TcShape {
     static constexpr int HALF = kBlock * 128;           // bytes: 128 rows of 64 BF16
     static constexpr int BLOCK = HALF * (D / 64);       // one block of K or V, or a query tile
     static constexpr int RING = I8 ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 8);
-    static constexpr int LOADERS = I8 ? 4 : 1;          // warps
-    static constexpr int THREADS = (8 + 1 + LOADERS) * 32;
+    // warpgroups: two of softmax, one of the MMA issuer (and the loader's warp), INT8: one of loaders
+    static constexpr int THREADS = I8 ? 512 : 384;
+    // registers a thread after the split; the shares add up to the launch's (512 x 128, 384 x 168)
+    static constexpr int REG_SOFTMAX = I8 ? 184 : 208, REG_ISSUE = I8 ? 56 : 88, REG_LOAD = 88;
     static constexpr int LD = D + 4;                    // floats a row of a partial state
     static constexpr int SCALES = I8 ? 2 * 16 * kBlock * 4 : 0;  // bytes: a block's K and V scales, by block number
 };
 
 struct Ctl {
-    uint64_t full[kMaxRing], empty[kMaxRing], fix, drain, q_ready[2], s_full[2], p_full[2], o_full[2];
+    uint64_t full[kMaxRing], empty[kMaxRing], fix, drain, q_ready[2], s_full[2], p_half[2], p_full[2], o_full[2];
     uint32_t tmem, abort;
     uint32_t mask[kMaskRing];    // pages of a key block that are there, by block number
     int seg_s, seg_h, seg_m;
@@ -89,23 +91,29 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lead) {
 __device__ __forceinline__ uint32_t idesc(int n, bool b_mn) {  // M 128, BF16 x BF16 -> FP32
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
+// Executed by a whole converged warp; one lane, the same one every time, issues.
+// (Issued from a branch that a single lane takes, an MMA cost 190-240 cycles
+// whatever its size, as its descriptors then live in ordinary registers; this way
+// 64 of M 128, N 128, K 16, the tensor core's rate.)
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(id), "r"(acc)
         : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(id), "r"(acc)
         : "memory");
 }
 __device__ __forceinline__ void commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -142,6 +150,38 @@ __device__ __forceinline__ void tst32(uint32_t t, const uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// two FP32 operations in one instruction
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// the lowest n bits
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; }
+
 // ------------------------------------------------------------------ the line of blocks
 // Pair m of (row, head): query rows 256 m .. of n G, the positions that some
 // row of it sees, as blocks: nhb of [0, head), the rest from block wb0 on.
@@ -153,8 +193,8 @@ __device__ __forceinline__ PairSpan pair_span(const AttnParams &p, const RowSpan
     const int r0 = m * kPair;
     a.rows = min(kPair, r.n * p.G - r0);
     const int base = r.len - r.n;
-    a.p_first = base + r0 / p.G;
-    a.p_last = base + (r0 + a.rows - 1) / p.G;
+    a.p_first = base + group_div(p, r0);
+    a.p_last = base + group_div(p, max(0, r0 + a.rows - 1));
     a.hi = max(0, a.p_last + 1);
     visible_span(p, a.hi, a.p_first, &a.head, &a.lo);
     a.nhb = (a.head + kBlock - 1) / kBlock;
@@ -263,6 +303,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->q_ready[i], 128);
             mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->p_half[i], 128);
             mbar_init(&ctl->p_full[i], 128);
             mbar_init(&ctl->o_full[i], 1);
         }
@@ -362,16 +403,16 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
         w.h = ctl->seg_h;
         w.m = ctl->seg_m;
         w.load(p);
-        long long at = ctl->seg_at, pos = begin;
+        const int start = (int)(begin - ctl->seg_at), work = (int)(end - begin);  // first block of the first pair, blocks
         auto block_of = [&](int b) { return b < w.a.nhb ? b : b - w.a.nhb + w.a.wb0; };
 
-        if (warp >= 9) {
-            // ================================================ loader
-            const int lt = tid - 9 * 32;  // thread of the loader
+        // ================================================ loader
+        auto loader = [&]() {
+            const int lt = tid - (I8 ? 12 : 9) * 32;  // thread of the loader
             int n = 0;                    // blocks of K and V so far
             uint32_t kb = 0, fixes = 0;   // key blocks, repaired blocks so far
-            while (pos < end && ok) {
-                const int b0 = (int)(pos - at), b1 = (int)min((long long)w.a.nb, end - at);
+            for (int b0 = start, left = work; left > 0 && ok; b0 = 0) {
+                const int b1 = min(w.a.nb, b0 + left);
                 const int32_t *table = c.tables + (size_t)w.s * c.width;
                 for (int b = b0; b < b1 && ok; ++b) {
                     const int t0 = block_of(b) * kBlock, npg = kBlock / c.ps;
@@ -467,92 +508,98 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     }
                     ++kb;
                 }
-                pos = at + b1;
-                if (pos < end) {
-                    at += w.a.nb;
-                    w.next(p);
-                }
+                left -= b1 - b0;
+                if (left > 0) w.next(p);
             }
             issued = n;
-        } else if (warp == 8) {
-            // ================================================ MMA issuer
-            if (lane == 0) {
-                const uint32_t id_s = idesc(kBlock, false), id_o = idesc(D, true);
-                const uint32_t o_tm = tmem + 256;
-                int n = 0;
-                uint32_t seg[2] = {0, 0}, step[2] = {0, 0};
-                auto s_mma = [&](int i, int st) {
-                    const uint64_t a = desc_k(smem_u32(sq + i * S::BLOCK)), b = desc_k(smem_u32(ring + st * S::BLOCK));
+        };
+        // ================================================ MMA issuer
+        auto issuer = [&]() {
+            const uint32_t id_s = idesc(kBlock, false), id_o = idesc(D, true);
+            const uint32_t o_tm = tmem + 256;
+            int n = 0;
+            uint32_t seg[2] = {0, 0}, step[2] = {0, 0};
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                ok = __all_sync(0xFFFFFFFFu, bounded_wait(bar, parity & 1u, deadline, abort));
+                fence_after();
+                return ok;
+            };
+            auto s_mma = [&](int i, int st) {
+                const uint64_t a = desc_k(smem_u32(sq + i * S::BLOCK)), b = desc_k(smem_u32(ring + st * S::BLOCK));
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t off = (uint64_t)((k / 4) * (S::HALF >> 4) + (k % 4) * 2);
-                        mma_ss(tmem + 128 * i, a + off, b + off, id_s, k != 0);
-                    }
-                    commit(&ctl->s_full[i]);
-                };
-                while (pos < end && ok) {
-                    const int b0 = (int)(pos - at), b1 = (int)min((long long)w.a.nb, end - at);
-                    const int nt = w.a.rows > kTile ? 2 : 1;
-                    ok = bounded_wait(&ctl->full[n % RING], (uint32_t)(n / RING) & 1u, deadline, abort);
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t off = (uint64_t)((k / 4) * (S::HALF >> 4) + (k % 4) * 2);
+                    mma_ss(tmem + 128 * i, a + off, b + off, id_s, k != 0);
+                }
+                commit(&ctl->s_full[i]);
+            };
+            for (int b0 = start, left = work; left > 0 && ok; b0 = 0) {
+                const int b1 = min(w.a.nb, b0 + left);
+                const int nt = w.a.rows > kTile ? 2 : 1;
+                if (!wait(&ctl->full[n % RING], (uint32_t)(n / RING))) break;
+                for (int i = 0; i < nt && ok; ++i) {
+                    if (!wait(&ctl->q_ready[i], seg[i])) break;
+                    ++seg[i];
+                    issued = 1;
+                    s_mma(i, n % RING);
+                }
+                if (!ok) break;
+                commit(&ctl->empty[n % RING]);
+                for (int b = b0; b < b1 && ok; ++b, n += 2) {
+                    const int sv = (n + 1) % RING, sk = (n + 2) % RING;
+                    if (!wait(&ctl->full[sv], (uint32_t)((n + 1) / RING))) break;
+                    const uint64_t bv = desc_mn(smem_u32(ring + sv * S::BLOCK), S::HALF);
                     for (int i = 0; i < nt && ok; ++i) {
-                        ok = bounded_wait(&ctl->q_ready[i], seg[i] & 1u, deadline, abort);
-                        if (!ok) break;
-                        ++seg[i];
-                        fence_after();
-                        issued = 1;
-                        s_mma(i, n % RING);
-                    }
-                    if (!ok) break;
-                    commit(&ctl->empty[n % RING]);
-                    for (int b = b0; b < b1 && ok; ++b, n += 2) {
-                        const int sv = (n + 1) % RING, sk = (n + 2) % RING;
-                        ok = bounded_wait(&ctl->full[sv], (uint32_t)((n + 1) / RING) & 1u, deadline, abort);
-                        if (!ok) break;
-                        for (int i = 0; i < nt && ok; ++i) {
-                            ok = bounded_wait(&ctl->p_full[i], step[i] & 1u, deadline, abort);
-                            if (!ok) break;
-                            ++step[i];
-                            fence_after();
-                            const uint64_t bv = desc_mn(smem_u32(ring + sv * S::BLOCK), S::HALF);
+                        // the weights come in two halves of 64 positions
 #pragma unroll
-                            for (int k = 0; k < kBlock / 16; ++k)
+                        for (int hf = 0; hf < 2; ++hf) {
+                            if (!wait(hf ? &ctl->p_full[i] : &ctl->p_half[i], step[i])) break;
+#pragma unroll
+                            for (int k = 4 * hf; k < 4 * hf + 4; ++k)
                                 mma_ts(o_tm + D * i, tmem + 128 * i + 8 * k, bv + (uint64_t)(k * (2048 >> 4)), id_o,
                                        b > b0 || k > 0);
-                            if (i == nt - 1) commit(&ctl->empty[sv]);
-                            if (b + 1 < b1) {
-                                if (i == 0) {
-                                    ok = bounded_wait(&ctl->full[sk], (uint32_t)((n + 2) / RING) & 1u, deadline, abort);
-                                    if (!ok) break;
-                                    fence_after();
-                                }
-                                s_mma(i, sk);
-                                if (i == nt - 1) commit(&ctl->empty[sk]);
-                            } else {
-                                commit(&ctl->o_full[i]);
-                            }
+                        }
+                        if (!ok) break;
+                        ++step[i];
+                        if (i == nt - 1) commit(&ctl->empty[sv]);
+                        if (b + 1 < b1) {
+                            if (i == 0 && !wait(&ctl->full[sk], (uint32_t)((n + 2) / RING))) break;
+                            s_mma(i, sk);
+                            if (i == nt - 1) commit(&ctl->empty[sk]);
+                        } else {
+                            commit(&ctl->o_full[i]);
                         }
                     }
-                    pos = at + b1;
-                    if (pos < end) {
-                        at += w.a.nb;
-                        w.next(p);
-                    }
                 }
+                left -= b1 - b0;
+                if (left > 0) w.next(p);
             }
-            __syncwarp();
+        };
+        // ================================================ softmax, one query row a thread
+        if (warp >= 12) {
+            if constexpr (I8) {
+                regs_down<S::REG_LOAD>();
+                loader();
+            }
+        } else if (warp >= 8) {
+            regs_down<S::REG_ISSUE>();
+            if (warp == 8)
+                issuer();
+            else if (!I8 && warp == 9)
+                loader();
         } else {
-            // ================================================ softmax, one query row a thread
+            regs_up<S::REG_SOFTMAX>();
             const int i = warp >> 2, row = tid & 127;
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
             const uint32_t s_tm = tmem + 128 * i + lanes, o_tm = tmem + 256 + D * i + lanes;
             uint32_t step = 0, seg = 0, kb = 0;
             uint32_t n = 0;  // ring blocks before the current key block
-            while (pos < end && ok) {
-                const int b0 = (int)(pos - at), b1 = (int)min((long long)w.a.nb, end - at);
+            for (int b0 = start, left = work; left > 0 && ok; b0 = 0) {
+                const int b1 = min(w.a.nb, b0 + left);
                 const int r = w.m * kPair + i * kTile + row;     // of the (sequence, KV head)
                 const bool mine_row = i * kTile + row < w.a.rows;
                 const bool tile_on = i * kTile < w.a.rows;
-                const int tok = r / p.G, hq = w.h * p.G + r % p.G;
+                const int tok = group_div(p, r), hq = w.h * p.G + r - tok * p.G;
                 const int lim = mine_row ? w.r.len - w.r.n + tok : -1;
                 if (tile_on) {
                     const uint16_t *q = p.q + (w.r.t0 + tok) * p.q_t + (long long)hq * p.q_h;
@@ -570,8 +617,8 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                 if (tile_on) {
                     // positions every row of the tile sees
                     const int ra = w.m * kPair + i * kTile, rz = min(ra + kTile, w.m * kPair + w.a.rows) - 1;
-                    const int all_hi = w.r.len - w.r.n + ra / p.G;
-                    const int all_lo = p.window > 0 ? w.r.len - w.r.n + rz / p.G - p.window + 1 : 0;
+                    const int all_hi = w.r.len - w.r.n + group_div(p, ra);
+                    const int all_lo = p.window > 0 ? w.r.len - w.r.n + group_div(p, rz) - p.window + 1 : 0;
                     for (int b = b0; b < b1; ++b, ++kb, n += 2) {
                         ok = bounded_wait(&ctl->s_full[i], step & 1u, deadline, abort);
                         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -590,12 +637,17 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                             for (int j = 0; j < kBlock; ++j) x(j) = __float_as_uint(__uint_as_float(x(j)) * ks[j]);
                         }
                         if (mask != 0xFFu || t0 + kBlock - 1 > all_hi || t0 < all_lo) {
+                            // a bit per position (what is seen is a range of the row and the sinks)
 #pragma unroll
-                            for (int j = 0; j < kBlock; ++j) {
-                                const int t = t0 + j;
-                                const bool see = t <= lim && (p.window == 0 || t > lim - p.window || t < p.sinks) &&
-                                                 ((mask >> (j / 16)) & 1u);
-                                if (!see) x(j) = 0xFF800000u;
+                            for (int k = 0; k < 4; ++k) {
+                                const int tb = t0 + 32 * k;
+                                uint32_t see = low_bits(lim + 1 - tb);
+                                if (p.window > 0)
+                                    see &= ~low_bits(lim - p.window + 1 - tb) | low_bits(p.sinks - tb);
+                                see &= ((mask >> (2 * k)) & 1u ? 0xFFFFu : 0u) | ((mask >> (2 * k + 1)) & 1u ? 0xFFFF0000u : 0u);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    if (!((see >> j) & 1u)) x(32 * k + j) = 0xFF800000u;
                             }
                         }
                         float bm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -603,7 +655,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                         for (int j = 0; j < kBlock; j += 8)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                bm[k] = fmaxf(bm[k], fmaxf(__uint_as_float(x(j + k)), __uint_as_float(x(j + 4 + k))));
+                                bm[k] = max3(bm[k], __uint_as_float(x(j + k)), __uint_as_float(x(j + 4 + k)));
                         const float top = fmaxf(fmaxf(bm[0], bm[1]), fmaxf(bm[2], bm[3])) * p.scale_log2;
                         const bool rise = top > mx + kRise || (mx == -INFINITY && top > mx);
                         if (__any_sync(0xFFFFFFFFu, rise)) {
@@ -623,7 +675,8 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                             }
                         }
                         const float base = mx == -INFINITY ? 0.f : mx;
-                        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                        const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2), nb2 = pack2(-base, -base);
+                        uint64_t ls[2] = {0ull, 0ull};  // sums of even and odd positions, two chains
                         const float *vs = nullptr;
                         if constexpr (I8) {
                             // the value block's scales: its copy is in once the block after the keys is full
@@ -638,10 +691,11 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
 #pragma unroll
                             for (int j = 0; j < 32; ++j) {
                                 const int k = hf * 64 + 2 * j;
-                                float e0 = ex2(fmaf(__uint_as_float(x(k)), p.scale_log2, -base));
-                                float e1 = ex2(fmaf(__uint_as_float(x(k + 1)), p.scale_log2, -base));
-                                ls[(2 * j) & 3] += e0;
-                                ls[(2 * j + 1) & 3] += e1;
+                                float e0, e1;
+                                unpack2(fma2(pack2(__uint_as_float(x(k)), __uint_as_float(x(k + 1))), sc2, nb2), e0, e1);
+                                e0 = ex2(e0);
+                                e1 = ex2(e1);
+                                ls[j & 1] = add2(ls[j & 1], pack2(e0, e1));
                                 if constexpr (I8) {
                                     e0 *= vs[k];
                                     e1 *= vs[k + 1];
@@ -649,12 +703,28 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                                 pk[j] = cvt_bf2(e0, e1);
                             }
                             tst32(s_tm + 32 * hf, pk);
+                            tst_wait();
+                            fence_before();
+                            mbar_arrive(hf ? &ctl->p_full[i] : &ctl->p_half[i]);
                         }
-                        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-                        tst_wait();
-                        fence_before();
-                        mbar_arrive(&ctl->p_full[i]);
+                        float l0, l1;
+                        unpack2(add2(ls[0], ls[1]), l0, l1);
+                        l += l0 + l1;
                     }
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                }
+                // the next pair, while the last product runs
+                Walk nx = w;
+                if (ok && left > b1 - b0) {
+                    nx.next(p);
+                    const int nr = nx.m * kPair + i * kTile + row, nt = group_div(p, nr);
+                    if (i * kTile + row < nx.a.rows) {
+                        const uint16_t *q = p.q + (nx.r.t0 + nt) * p.q_t + (long long)(nx.h * p.G + nr - nt * p.G) * p.q_h;
+                        prefetch_l2(q);
+                        if (D == 128) prefetch_l2(q + 64);
+                    }
+                }
+                if (tile_on) {
                     // ---- the pair's output, or this piece's state
                     ok = ok && bounded_wait(&ctl->o_full[i], seg & 1u, deadline, abort);
                     ok = __all_sync(0xFFFFFFFFu, ok);
@@ -662,7 +732,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     ++seg;
                     fence_after();
                     const bool whole = b0 == 0 && b1 == w.a.nb;
-                    const int slot = pos == begin ? 0 : 1;
+                    const int slot = left == work ? 0 : 1;
                     if (whole) {
                         const float inv = l == 0.f ? 0.f : 1.f / l;
                         bool finite = true;
@@ -707,7 +777,8 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                         if (mine_row) *reinterpret_cast<float2 *>(dst + D) = make_float2(mx, l);
                         if (b0 == 0 && tid == 0) {
                             SegRec rec;
-                            rec.parts = (int)(((at + w.a.nb) * nc + total - 1) / total - 1 - cta) + 1;
+                            // the CTA that has the pair's last block
+                            rec.parts = (int)(((begin + (work - left) + w.a.nb) * nc + total - 1) / total - 1 - cta) + 1;
                             rec.s = w.s;
                             rec.h = w.h;
                             rec.m = w.m;
@@ -720,11 +791,8 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     kb += (uint32_t)(b1 - b0);
                     n += 2u * (uint32_t)(b1 - b0);
                 }
-                pos = at + b1;
-                if (pos < end) {
-                    at += w.a.nb;
-                    w.next(p);
-                }
+                left -= b1 - b0;
+                w = nx;
             }
         }
     }
@@ -748,7 +816,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
         if (lane == 0) atomicOr(reinterpret_cast<uint32_t *>(c.state), kDevTimeout);
         const unsigned long long d2 = global_timer() + kTimeoutNs;
         uint32_t never = 0;
-        if (warp == 8 && lane == 0 && issued) {
+        if (warp == 8 && issued) {
             commit(&ctl->drain);
             bounded_wait(&ctl->drain, 0u, d2, &never);
         }

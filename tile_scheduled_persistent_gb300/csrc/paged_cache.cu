@@ -688,7 +688,8 @@ tiles_status_t tiles_paged_attention(const tiles_paged_cache *cache, int32_t lay
         max_tokens < 1 || window < 0 || sinks < 0 || !(scale > 0.f) || scale > 1e30f || !al4(cu_tokens) ||
         (!cu_tokens && n_tokens != d.n_seqs))
         return TILES_ERR_INVALID_ARG;
-    if (n_q_heads / d.n_kv_heads > 16) return TILES_ERR_UNSUPPORTED;
+    if (n_q_heads / d.n_kv_heads > 16 || (long long)n_tokens * (n_q_heads / d.n_kv_heads) >= (1ll << 28))
+        return TILES_ERR_UNSUPPORTED;
     if (n_tokens == 0) return TILES_OK;
     if (!q || !out || !al16(q) || !al16(out) || q_stride_token % 8 || q_stride_head % 8 || out_stride_token % 8 ||
         out_stride_head % 8 || !workspace || !al16(workspace))
@@ -709,6 +710,7 @@ tiles_status_t tiles_paged_attention(const tiles_paged_cache *cache, int32_t lay
     p.n_tokens = n_tokens;
     p.max_tokens = max_tokens;
     p.G = n_q_heads / d.n_kv_heads;
+    p.g_mul = (unsigned)(((1ull << 32) + (unsigned)p.G - 1) / (unsigned)p.G);
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     p.window = window;
     p.sinks = window > 0 ? sinks : 0;

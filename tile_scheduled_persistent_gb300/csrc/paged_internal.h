@@ -40,11 +40,18 @@ struct AttnParams {
     long long q_t, q_h, o_t, o_h;  // strides in elements
     const int32_t *cu;             // null: one token a row
     int n_tokens, max_tokens, G;
+    unsigned g_mul;                // ceil(2^32 / G): see group_div
     float scale_log2;              // scale * log2(e): the softmax runs on powers of two
     int window, sinks;
     float *ws;
     int ctas;                      // CTAs that share the work
 };
+
+// x / G for 0 <= x < 2^28: g_mul = (2^32 + e) / G with 0 <= e < G <= 16, so the
+// product's error x e / 2^32 stays below 1 / G.
+__device__ __forceinline__ int group_div(const AttnParams &p, int x) {
+    return p.G == 1 ? x : (int)__umulhi((unsigned)x, p.g_mul);
+}
 
 // Row s's tokens in the call (first token, count) and its length; a row that
 // breaks the rules (token offsets out of order or range, more than max_tokens)
