@@ -625,3 +625,19 @@ def test_repeated_calls_are_bitwise_equal(tsp):
     c = Case(tsp, [2000, 40, 700], [300, 40, 99], 4, 2, 64, 16, seed=34)
     a = c.run()
     assert all(torch.equal(a, c.run()) for _ in range(5))
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_runs_are_bitwise_equal(tsp, d, i8):
+    """Split, joined and whole pieces, 200 times, with a cold L2 every other time: a
+    missing wait between the kernel's roles shows as a bit that changes."""
+    import torch
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    for lens, ns in (([5003], [17]), ([2000, 40, 700], [300, 40, 99]), ([900, 3000], [1, 1])):
+        c = Case(tsp, lens, ns, 4, 1, d, 16, i8, seed=35)
+        first = c.run()
+        for i in range(200):
+            if i % 2:
+                flush.fill_(i)
+            assert torch.equal(first, c.run()), i

@@ -18,8 +18,10 @@
 //     when the softmax has turned S_i into weights in place, O_i += P_i V with P_i
 //     read from tensor memory. While one tile's rows are in the softmax the tensor
 //     cores work on the other tile.
-//   - a softmax warpgroup per tile, one row a thread: running maximum and sum in
-//     FP32, no shuffles. O_i is rescaled only when a row's maximum has risen by
+//   - two softmax warpgroups per tile, half a row of a block a thread: running
+//     maximum and sum in FP32; the halves exchange their maxima through shared memory.
+//     (One warpgroup, a row a thread: the chain from scores to weights took 1,700
+//     cycles and the tensor cores waited for it.) O_i is rescaled only when a row's maximum has risen by
 //     more than 8 powers of two since it was last set (weights stay below 2^8,
 //     which neither BF16 nor the FP32 sums mind), so hardly ever after the first
 //     block.
@@ -49,27 +51,31 @@ constexpr int kPair = 2 * kTile; // query rows a CTA works on at a time
 constexpr int kMaxRing = 8;
 constexpr int kMaskRing = 16;
 constexpr unsigned long long kTimeoutNs = 2000000000ull;
+// The line in which the work is cut counts a pair as its blocks and kPairCost
+// blocks' time for its queries, its output and the change from one to the next.
+constexpr int kPairCost = 3;
 constexpr float kRise = 8.0f;    // powers of two a maximum may rise before O is rescaled
 
 template <int D, bool I8>
 struct TcShape {
     static constexpr int HALF = kBlock * 128;           // bytes: 128 rows of 64 BF16
     static constexpr int BLOCK = HALF * (D / 64);       // one block of K or V, or a query tile
-    static constexpr int RING = I8 ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 8);
-    // warpgroups: two of softmax, one of the MMA issuer (and the loader's warp), INT8: one of loaders
-    static constexpr int THREADS = I8 ? 512 : 384;
-    // registers a thread after the split; the shares add up to the launch's (512 x 128, 384 x 168)
-    static constexpr int REG_SOFTMAX = I8 ? 184 : 208, REG_ISSUE = I8 ? 56 : 88, REG_LOAD = 88;
+    static constexpr int RING = D == 128 ? 4 : 8;
+    // warpgroups: four of softmax, one of the MMA issuer and the loader
+    static constexpr int THREADS = 640, LOADERS = I8 ? 96 : 32;
+    // registers a thread after the split: 4 x 104 + 64 = 5 x 96, the launch's
+    static constexpr int REG_SOFTMAX = 104, REG_ISSUE = 64;
     static constexpr int LD = D + 4;                    // floats a row of a partial state
     static constexpr int SCALES = I8 ? 2 * 16 * kBlock * 4 : 0;  // bytes: a block's K and V scales, by block number
 };
 
 struct Ctl {
-    uint64_t full[kMaxRing], empty[kMaxRing], fix, drain, q_ready[2], s_full[2], p_half[2], p_full[2], o_full[2];
+    uint64_t full[kMaxRing], empty[kMaxRing], fix, drain, q_ready[2], s_full[2], p_full[2], o_full[2], x_ready[2][4];
     uint32_t tmem, abort;
     uint32_t mask[kMaskRing];    // pages of a key block that are there, by block number
     int seg_s, seg_h, seg_m;
-    long long seg_at, scan[16];
+    long long seg_at, scan[20];
+    float top[4][2][2][kTile];   // row maxima of the last four blocks, of a tile's halves (the sums, at a pair's end)
 };
 
 struct SegRec {
@@ -120,16 +126,7 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 
 #define R8(a, o) "=r"(a[o]), "=r"(a[o + 1]), "=r"(a[o + 2]), "=r"(a[o + 3]), "=r"(a[o + 4]), "=r"(a[o + 5]), "=r"(a[o + 6]), "=r"(a[o + 7])
 #define V8(a, o) "r"(a[o]), "r"(a[o + 1]), "r"(a[o + 2]), "r"(a[o + 3]), "r"(a[o + 4]), "r"(a[o + 5]), "r"(a[o + 6]), "r"(a[o + 7])
-// 32 consecutive columns of this thread's tensor-memory lane, complete on return
-__device__ __forceinline__ void tld32(uint32_t t, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24)
-        : "r"(t)
-        : "memory");
-}
+// 64, or 16, consecutive columns of this thread's tensor-memory lane, complete on return
 __device__ __forceinline__ void tld64(uint32_t t, uint32_t (&r)[64]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -141,11 +138,19 @@ __device__ __forceinline__ void tld64(uint32_t t, uint32_t (&r)[64]) {
         : "r"(t)
         : "memory");
 }
-__device__ __forceinline__ void tst32(uint32_t t, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tld16(uint32_t t, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(t),
-        V8(r, 0), V8(r, 8), V8(r, 16), V8(r, 24)
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : R8(r, 0), R8(r, 8)
+        : "r"(t)
+        : "memory");
+}
+__device__ __forceinline__ void tst16(uint32_t t, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(t),
+        V8(r, 0), V8(r, 8)
         : "memory");
 }
 __device__ __forceinline__ void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -187,6 +192,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 
 // row of it sees, as blocks: nhb of [0, head), the rest from block wb0 on.
 struct PairSpan {
     int rows, p_first, p_last, head, lo, hi, nhb, wb0, nb;
+    __device__ __forceinline__ int cost() const { return nb ? nb + kPairCost : 0; }
 };
 __device__ __forceinline__ PairSpan pair_span(const AttnParams &p, const RowSpan &r, int m) {
     PairSpan a;
@@ -205,11 +211,11 @@ __device__ __forceinline__ PairSpan pair_span(const AttnParams &p, const RowSpan
 }
 __device__ __forceinline__ int pairs_of(const AttnParams &p, const RowSpan &r) { return (r.n * p.G + kPair - 1) / kPair; }
 
-// Blocks of one head of each of 32 rows (one a lane): rows of several pairs are
+// Cost of one head of each of 32 rows (one a lane): rows of several pairs are
 // added up by the whole warp.
-__device__ __forceinline__ int row_blocks(const AttnParams &p, const RowSpan &r, int lane) {
+__device__ __forceinline__ int row_cost(const AttnParams &p, const RowSpan &r, int lane) {
     const int np = pairs_of(p, r);
-    int nb = np == 1 ? pair_span(p, r, 0).nb : 0;
+    int nb = np == 1 ? pair_span(p, r, 0).cost() : 0;
     uint32_t many = __ballot_sync(0xFFFFFFFFu, np > 1);
     while (many) {
         const int src = __ffs(many) - 1;
@@ -220,7 +226,7 @@ __device__ __forceinline__ int row_blocks(const AttnParams &p, const RowSpan &r,
         q.len = __shfl_sync(0xFFFFFFFFu, r.len, src);
         const int k = pairs_of(p, q);
         int sum = 0;
-        for (int m = lane; m < k; m += 32) sum += pair_span(p, q, m).nb;
+        for (int m = lane; m < k; m += 32) sum += pair_span(p, q, m).cost();
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         if (lane == src) nb = sum;
@@ -295,16 +301,16 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
     if (tid == 0) {
         recs[cta].parts = 0;
         for (int i = 0; i < RING; ++i) {
-            mbar_init(&ctl->full[i], I8 ? 128 : 1);
+            mbar_init(&ctl->full[i], I8 ? S::LOADERS : 1);
             mbar_init(&ctl->empty[i], 1);
         }
         mbar_init(&ctl->fix, 1);
         mbar_init(&ctl->drain, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&ctl->q_ready[i], 128);
+            mbar_init(&ctl->q_ready[i], 256);
             mbar_init(&ctl->s_full[i], 1);
-            mbar_init(&ctl->p_half[i], 128);
-            mbar_init(&ctl->p_full[i], 128);
+            mbar_init(&ctl->p_full[i], 256);
+            for (int k = 0; k < 4; ++k) mbar_init(&ctl->x_ready[i][k], 64);
             mbar_init(&ctl->o_full[i], 1);
         }
         ctl->abort = 0;
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
         RowSpan r = {0, 0, 0};
         bool bad = false;
         if (s0 + lane < sb) r = row_span(p, s0 + lane, &bad);
-        mine += row_blocks(p, r, lane);
+        mine += row_cost(p, r, lane);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
@@ -329,7 +335,8 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
         if (w < warp) before += ctl->scan[w];
         total += ctl->scan[w];
     }
-    const long long nc = min((long long)p.ctas, total);
+    // pieces of at least one block and its pair's cost
+    const long long nc = min((long long)p.ctas, max(1ll, total / (kPairCost + 1)));
     const long long begin = cta < nc ? cta * total / nc : 0, end = cta < nc ? (cta + 1) * total / nc : 0;
     if (begin < end && begin >= before && begin < before + mine) {
         // the row, then the head, then the pair that holds block `begin`
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             RowSpan r = {0, 0, 0};
             bool bad = false;
             if (s0 + lane < sb) r = row_span(p, s0 + lane, &bad);
-            const int nb = row_blocks(p, r, lane);
+            const int nb = row_cost(p, r, lane);
             long long x = (long long)nb * c.nkv;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -359,7 +366,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                 long long pos = row_at + (long long)h * row_nb;
                 const int np = pairs_of(p, q);
                 for (int m0 = 0; m0 < np; m0 += 32) {
-                    int k = m0 + lane < np ? pair_span(p, q, m0 + lane).nb : 0, y = k;
+                    int k = m0 + lane < np ? pair_span(p, q, m0 + lane).cost() : 0, y = k;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
                         const int z = __shfl_up_sync(0xFFFFFFFFu, y, o);
@@ -403,16 +410,30 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
         w.h = ctl->seg_h;
         w.m = ctl->seg_m;
         w.load(p);
-        const int start = (int)(begin - ctl->seg_at), work = (int)(end - begin);  // first block of the first pair, blocks
+        // in cost units: where the piece begins in its first pair, how long it is. Of a pair that
+        // begins at unit 0, units kPairCost + b are block b.
+        const int start = (int)(begin - ctl->seg_at), work = (int)(end - begin);
+        struct Piece {
+            int b0, b1, used;
+        };
+        auto piece_of = [&](int at, int left) {
+            Piece r;
+            r.used = min(w.a.cost() - at, left);
+            r.b0 = max(0, at - kPairCost);
+            r.b1 = max(0, at + r.used - kPairCost);
+            return r;
+        };
         auto block_of = [&](int b) { return b < w.a.nhb ? b : b - w.a.nhb + w.a.wb0; };
 
         // ================================================ loader
         auto loader = [&]() {
-            const int lt = tid - (I8 ? 12 : 9) * 32;  // thread of the loader
+            const int lt = tid - 17 * 32;  // thread of the loader
             int n = 0;                    // blocks of K and V so far
             uint32_t kb = 0, fixes = 0;   // key blocks, repaired blocks so far
-            for (int b0 = start, left = work; left > 0 && ok; b0 = 0) {
-                const int b1 = min(w.a.nb, b0 + left);
+            for (int at = start, left = work; left > 0 && ok; at = 0) {
+                const Piece pc = piece_of(at, left);
+                const int b0 = pc.b0, b1 = pc.b1;
+                left -= pc.used;
                 const int32_t *table = c.tables + (size_t)w.s * c.width;
                 for (int b = b0; b < b1 && ok; ++b) {
                     const int t0 = block_of(b) * kBlock, npg = kBlock / c.ps;
@@ -472,34 +493,42 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                             // 16 codes a step: a row is D / 16 steps
                             const uint8_t *pool = kv ? c.v : c.k;
                             const float *scales = kv ? c.vs : c.ks;
-                            constexpr int UPR = D / 16, STEPS = kBlock * UPR / 128;
-                            uint4 w4[STEPS];
-#pragma unroll
-                            for (int k = 0; k < STEPS; ++k) {
-                                const int i = lt + 128 * k, row = i / UPR, u = i % UPR;
-                                const int pg = __shfl_sync(0xFFFFFFFFu, page, row >> c.psl);
-                                w4[k] = make_uint4(0u, 0u, 0u, 0u);
-                                if (pg >= 0 && (kv == 0 || t0 + row < w.a.hi))
-                                    w4[k] = __ldg(reinterpret_cast<const uint4 *>(
-                                        pool + (((size_t)pg * c.nkv + w.h) * c.ps + (row & (c.ps - 1))) * D + 16 * u));
+                            constexpr int UPR = D / 16, UNITS = kBlock * UPR;
+                            constexpr int STEPS = (UNITS + S::LOADERS - 1) / S::LOADERS, AT_ONCE = 4;
+                            for (int r = lt; r < kBlock + S::LOADERS; r += S::LOADERS) {
+                                const int pg = __shfl_sync(0xFFFFFFFFu, page, (r & (kBlock - 1)) >> c.psl);
+                                if (r >= kBlock) break;
+                                float f = 0.f;
+                                if (pg >= 0 && t0 + r < w.a.hi)
+                                    f = __ldg(scales + ((size_t)pg * c.nkv + w.h) * c.ps + (r & (c.ps - 1)));
+                                scale[kv][kb % kMaskRing][r] = f;
                             }
-                            const int pg = __shfl_sync(0xFFFFFFFFu, page, lt >> c.psl);  // of this thread's row
-                            float f = 0.f;
-                            if (pg >= 0 && t0 + lt < w.a.hi)
-                                f = __ldg(scales + ((size_t)pg * c.nkv + w.h) * c.ps + (lt & (c.ps - 1)));
-                            scale[kv][kb % kMaskRing][lt] = f;
+                            __syncwarp();
+                            for (int k0 = 0; k0 < STEPS; k0 += AT_ONCE) {
+                                uint4 w4[AT_ONCE];
 #pragma unroll
-                            for (int k = 0; k < STEPS; ++k) {
-                                const int i = lt + 128 * k, row = i / UPR, u = i % UPR;
-                                const uint32_t x[4] = {w4[k].x, w4[k].y, w4[k].z, w4[k].w};
-                                uint32_t y[8];
+                                for (int k = 0; k < AT_ONCE; ++k) {
+                                    const int i = lt + S::LOADERS * (k0 + k), row = (i / UPR) & (kBlock - 1), u = i % UPR;
+                                    const int pg = __shfl_sync(0xFFFFFFFFu, page, row >> c.psl);
+                                    w4[k] = make_uint4(0u, 0u, 0u, 0u);
+                                    if (i < UNITS && pg >= 0 && (kv == 0 || t0 + row < w.a.hi))
+                                        w4[k] = __ldg(reinterpret_cast<const uint4 *>(
+                                            pool + (((size_t)pg * c.nkv + w.h) * c.ps + (row & (c.ps - 1))) * D + 16 * u));
+                                }
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) codes_bf16x2(x[j], y[2 * j], y[2 * j + 1]);
+                                for (int k = 0; k < AT_ONCE; ++k) {
+                                    const int i = lt + S::LOADERS * (k0 + k), row = i / UPR, u = i % UPR;
+                                    if (i >= UNITS) break;
+                                    const uint32_t x[4] = {w4[k].x, w4[k].y, w4[k].z, w4[k].w};
+                                    uint32_t y[8];
 #pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    const int uu = 2 * u + j;
-                                    *reinterpret_cast<uint4 *>(dst + (uu / 8) * S::HALF + row * 128 + (((uu % 8) ^ (row & 7)) << 4)) =
-                                        make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                                    for (int j = 0; j < 4; ++j) codes_bf16x2(x[j], y[2 * j], y[2 * j + 1]);
+#pragma unroll
+                                    for (int j = 0; j < 2; ++j) {
+                                        const int uu = 2 * u + j;
+                                        *reinterpret_cast<uint4 *>(dst + (uu / 8) * S::HALF + row * 128 + (((uu % 8) ^ (row & 7)) << 4)) =
+                                            make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                                    }
                                 }
                             }
                             fence_proxy_async_smem();
@@ -508,7 +537,6 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     }
                     ++kb;
                 }
-                left -= b1 - b0;
                 if (left > 0) w.next(p);
             }
             issued = n;
@@ -533,9 +561,15 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                 }
                 commit(&ctl->s_full[i]);
             };
-            for (int b0 = start, left = work; left > 0 && ok; b0 = 0) {
-                const int b1 = min(w.a.nb, b0 + left);
+            for (int at = start, left = work; left > 0 && ok; at = 0) {
+                const Piece pc = piece_of(at, left);
+                const int b0 = pc.b0, b1 = pc.b1;
+                left -= pc.used;
                 const int nt = w.a.rows > kTile ? 2 : 1;
+                if (b0 >= b1) {  // only the pair's first cost units: the next CTA begins it
+                    if (left > 0) w.next(p);
+                    continue;
+                }
                 if (!wait(&ctl->full[n % RING], (uint32_t)(n / RING))) break;
                 for (int i = 0; i < nt && ok; ++i) {
                     if (!wait(&ctl->q_ready[i], seg[i])) break;
@@ -550,16 +584,10 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     if (!wait(&ctl->full[sv], (uint32_t)((n + 1) / RING))) break;
                     const uint64_t bv = desc_mn(smem_u32(ring + sv * S::BLOCK), S::HALF);
                     for (int i = 0; i < nt && ok; ++i) {
-                        // the weights come in two halves of 64 positions
+                        if (!wait(&ctl->p_full[i], step[i])) break;
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            if (!wait(hf ? &ctl->p_full[i] : &ctl->p_half[i], step[i])) break;
-#pragma unroll
-                            for (int k = 4 * hf; k < 4 * hf + 4; ++k)
-                                mma_ts(o_tm + D * i, tmem + 128 * i + 8 * k, bv + (uint64_t)(k * (2048 >> 4)), id_o,
-                                       b > b0 || k > 0);
-                        }
-                        if (!ok) break;
+                        for (int k = 0; k < kBlock / 16; ++k)
+                            mma_ts(o_tm + D * i, tmem + 128 * i + 64 * (k / 4) + 8 * (k % 4), bv + (uint64_t)(k * (2048 >> 4)), id_o, b > b0 || k > 0);
                         ++step[i];
                         if (i == nt - 1) commit(&ctl->empty[sv]);
                         if (b + 1 < b1) {
@@ -571,41 +599,52 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                         }
                     }
                 }
-                left -= b1 - b0;
                 if (left > 0) w.next(p);
             }
         };
-        // ================================================ softmax, one query row a thread
-        if (warp >= 12) {
-            if constexpr (I8) {
-                regs_down<S::REG_LOAD>();
-                loader();
-            }
-        } else if (warp >= 8) {
+        // ================================================ softmax, half a query row a thread
+        if (warp >= 16) {
             regs_down<S::REG_ISSUE>();
-            if (warp == 8)
+            if (warp == 16)
                 issuer();
-            else if (!I8 && warp == 9)
+            else if (I8 || warp == 17)
                 loader();
         } else {
             regs_up<S::REG_SOFTMAX>();
-            const int i = warp >> 2, row = tid & 127;
+            const int i = warp >> 3, half = (warp >> 2) & 1, row = tid & 127;
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-            const uint32_t s_tm = tmem + 128 * i + lanes, o_tm = tmem + 256 + D * i + lanes;
+            // this thread's scores, and its weights in place of them (not of the other half's, whose
+            // thread may still be reading); its part of O
+            const uint32_t s_tm = tmem + 128 * i + 64 * half + lanes, p_tm = s_tm;
+            const uint32_t o_tm = tmem + 256 + D * i + D / 2 * half + lanes;
+            uint64_t *x_ready = &ctl->x_ready[i][warp & 3];
+            auto top_of = [&](uint32_t block, int h) -> volatile float & { return ctl->top[block & 3][i][h][row]; };
+            uint32_t xs = 0;  // exchanges with the other half so far
+            auto exchange = [&](uint32_t block, float v) {
+                top_of(block, half) = v;
+                mbar_arrive(x_ready);
+                ok = __all_sync(0xFFFFFFFFu, bounded_wait(x_ready, xs & 1u, deadline, abort));
+                ++xs;
+                return top_of(block, half ^ 1);
+            };
             uint32_t step = 0, seg = 0, kb = 0;
+            bool first = true;  // no pair with blocks so far
             uint32_t n = 0;  // ring blocks before the current key block
-            for (int b0 = start, left = work; left > 0 && ok; b0 = 0) {
-                const int b1 = min(w.a.nb, b0 + left);
+            for (int at = start, left = work; left > 0 && ok; at = 0) {
+                const Piece pc = piece_of(at, left);
+                const int b0 = pc.b0, b1 = pc.b1;
+                left -= pc.used;
                 const int r = w.m * kPair + i * kTile + row;     // of the (sequence, KV head)
                 const bool mine_row = i * kTile + row < w.a.rows;
-                const bool tile_on = i * kTile < w.a.rows;
+                const bool tile_on = i * kTile < w.a.rows && b0 < b1;
                 const int tok = group_div(p, r), hq = w.h * p.G + r - tok * p.G;
                 const int lim = mine_row ? w.r.len - w.r.n + tok : -1;
                 if (tile_on) {
                     const uint16_t *q = p.q + (w.r.t0 + tok) * p.q_t + (long long)hq * p.q_h;
                     uint8_t *dst = sq + i * S::BLOCK + row * 128;
 #pragma unroll
-                    for (int u = 0; u < D / 8; ++u) {
+                    for (int v = 0; v < D / 16; ++v) {
+                        const int u = D / 16 * half + v;
                         uint4 x = make_uint4(0u, 0u, 0u, 0u);
                         if (mine_row) x = __ldg(reinterpret_cast<const uint4 *>(q + 8 * u));
                         *reinterpret_cast<uint4 *>(dst + (u / 8) * S::HALF + (((u % 8) ^ (row & 7)) << 4)) = x;
@@ -613,7 +652,8 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     fence_proxy_async_smem();
                     mbar_arrive(&ctl->q_ready[i]);
                 }
-                float mx = -INFINITY, l = 0.f;
+                // rows that see nothing need no maximum
+                float mx = lim < 0 ? 0.f : -INFINITY, l = 0.f, top1 = -INFINITY, top2 = -INFINITY;
                 if (tile_on) {
                     // positions every row of the tile sees
                     const int ra = w.m * kPair + i * kTile, rz = min(ra + kTile, w.m * kPair + w.a.rows) - 1;
@@ -625,21 +665,25 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                         if (!ok) break;
                         ++step;
                         fence_after();
-                        const int t0 = block_of(b) * kBlock;
-                        const uint32_t mask = ctl->mask[kb % kMaskRing];
-                        uint32_t s0[64], s1[64];
-                        tld64(s_tm, s0);
-                        tld64(s_tm + 64, s1);
-                        auto x = [&](int j) -> uint32_t & { return j < 64 ? s0[j] : s1[j - 64]; };
+                        const int t0 = block_of(b) * kBlock + 64 * half;  // of this thread's positions
+                        const uint32_t mask = ctl->mask[kb % kMaskRing] >> (4 * half);
+                        uint32_t x[64];
+                        tld64(s_tm, x);
                         if constexpr (I8) {
-                            const float *ks = scale[0][kb % kMaskRing];
+                            const float4 *ks = reinterpret_cast<const float4 *>(scale[0][kb % kMaskRing] + 64 * half);
 #pragma unroll
-                            for (int j = 0; j < kBlock; ++j) x(j) = __float_as_uint(__uint_as_float(x(j)) * ks[j]);
+                            for (int j = 0; j < 16; ++j) {
+                                const float4 f = ks[j];
+                                x[4 * j] = __float_as_uint(__uint_as_float(x[4 * j]) * f.x);
+                                x[4 * j + 1] = __float_as_uint(__uint_as_float(x[4 * j + 1]) * f.y);
+                                x[4 * j + 2] = __float_as_uint(__uint_as_float(x[4 * j + 2]) * f.z);
+                                x[4 * j + 3] = __float_as_uint(__uint_as_float(x[4 * j + 3]) * f.w);
+                            }
                         }
-                        if (mask != 0xFFu || t0 + kBlock - 1 > all_hi || t0 < all_lo) {
+                        if ((mask & 0xFu) != 0xFu || t0 + 63 > all_hi || t0 < all_lo) {
                             // a bit per position (what is seen is a range of the row and the sinks)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
+                            for (int k = 0; k < 2; ++k) {
                                 const int tb = t0 + 32 * k;
                                 uint32_t see = low_bits(lim + 1 - tb);
                                 if (p.window > 0)
@@ -647,30 +691,42 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                                 see &= ((mask >> (2 * k)) & 1u ? 0xFFFFu : 0u) | ((mask >> (2 * k + 1)) & 1u ? 0xFFFF0000u : 0u);
 #pragma unroll
                                 for (int j = 0; j < 32; ++j)
-                                    if (!((see >> j) & 1u)) x(32 * k + j) = 0xFF800000u;
+                                    if (!((see >> j) & 1u)) x[32 * k + j] = 0xFF800000u;
                             }
                         }
-                        float bm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        auto block_top = [&]() {
+                            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int j = 0; j < kBlock; j += 8)
+                            for (int j = 0; j < 64; j += 8)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                bm[k] = max3(bm[k], __uint_as_float(x(j + k)), __uint_as_float(x(j + 4 + k)));
-                        const float top = fmaxf(fmaxf(bm[0], bm[1]), fmaxf(bm[2], bm[3])) * p.scale_log2;
-                        const bool rise = top > mx + kRise || (mx == -INFINITY && top > mx);
-                        if (__any_sync(0xFFFFFFFFu, rise)) {
-                            const float nm = rise ? top : mx;
+                                for (int k = 0; k < 4; ++k)
+                                    m4[k] = max3(m4[k], __uint_as_float(x[j + k]), __uint_as_float(x[j + 4 + k]));
+                            return max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * p.scale_log2;
+                        };
+                        // the row's reference: what both halves had seen two blocks ago
+                        float nm = mx;
+                        if (b - b0 >= 2) {
+                            const float t = fmaxf(top2, top_of(kb + 2, half ^ 1));
+                            if (t > mx + kRise) nm = t;
+                        }
+                        if (__any_sync(0xFFFFFFFFu, mx == -INFINITY)) {  // rows that have seen nothing yet
+                            const float t = block_top(), u = fmaxf(t, exchange(kb, t));
+                            if (!ok) break;
+                            if (mx == -INFINITY) nm = u;
+                        }
+                        if (__any_sync(0xFFFFFFFFu, nm > mx)) {
                             const float corr = nm > mx ? ex2(mx - nm) : 1.f;
                             mx = nm;
                             l *= corr;
                             if (b > b0) {
                                 // the last P V is complete: it was issued before this block's S
-                                for (int d = 0; d < D; d += 32) {
-                                    uint32_t o[32];
-                                    tld32(o_tm + d, o);
+#pragma unroll 1
+                                for (int d = 0; d < D / 2; d += 16) {
+                                    uint32_t o[16];
+                                    tld16(o_tm + d, o);
 #pragma unroll
-                                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
-                                    tst32(o_tm + d, o);
+                                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+                                    tst16(o_tm + d, o);
                                 }
                             }
                         }
@@ -680,42 +736,46 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                         const float *vs = nullptr;
                         if constexpr (I8) {
                             // the value block's scales: its copy is in once the block after the keys is full
-                            ok = bounded_wait(&ctl->full[(n + 1) % RING], ((n + 1) / RING) & 1u, deadline, abort);
-                            ok = __all_sync(0xFFFFFFFFu, ok);
+                            ok = __all_sync(0xFFFFFFFFu, bounded_wait(&ctl->full[(n + 1) % RING], ((n + 1) / RING) & 1u, deadline, abort));
                             if (!ok) break;
-                            vs = scale[1][kb % kMaskRing];
+                            vs = scale[1][kb % kMaskRing] + 64 * half;
                         }
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            uint32_t pk[32];
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t pk[16];
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const int k = hf * 64 + 2 * j;
+                            for (int j = 0; j < 16; ++j) {
+                                const int k = q * 32 + 2 * j;
                                 float e0, e1;
-                                unpack2(fma2(pack2(__uint_as_float(x(k)), __uint_as_float(x(k + 1))), sc2, nb2), e0, e1);
+                                unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), sc2, nb2), e0, e1);
                                 e0 = ex2(e0);
                                 e1 = ex2(e1);
                                 ls[j & 1] = add2(ls[j & 1], pack2(e0, e1));
                                 if constexpr (I8) {
-                                    e0 *= vs[k];
-                                    e1 *= vs[k + 1];
+                                    const float2 f = *reinterpret_cast<const float2 *>(vs + k);
+                                    e0 *= f.x;
+                                    e1 *= f.y;
                                 }
                                 pk[j] = cvt_bf2(e0, e1);
                             }
-                            tst32(s_tm + 32 * hf, pk);
-                            tst_wait();
-                            fence_before();
-                            mbar_arrive(hf ? &ctl->p_full[i] : &ctl->p_half[i]);
+                            tst16(p_tm + 16 * q, pk);
                         }
+                        tst_wait();
+                        fence_before();
+                        mbar_arrive(&ctl->p_full[i]);
+                        // off the path to the next product
                         float l0, l1;
                         unpack2(add2(ls[0], ls[1]), l0, l1);
                         l += l0 + l1;
+                        top2 = top1;
+                        top1 = block_top();
+                        top_of(kb, half) = top1;
                     }
                     ok = __all_sync(0xFFFFFFFFu, ok);
                 }
                 // the next pair, while the last product runs
                 Walk nx = w;
-                if (ok && left > b1 - b0) {
+                if (ok && left > 0) {
                     nx.next(p);
                     const int nr = nx.m * kPair + i * kTile + row, nt = group_div(p, nr);
                     if (i * kTile + row < nx.a.rows) {
@@ -731,18 +791,21 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     if (!ok) break;
                     ++seg;
                     fence_after();
+                    const float l_all = l + exchange(kb, l);
+                    if (!ok) break;
                     const bool whole = b0 == 0 && b1 == w.a.nb;
-                    const int slot = left == work ? 0 : 1;
+                    const int slot = first ? 0 : 1;
                     if (whole) {
-                        const float inv = l == 0.f ? 0.f : 1.f / l;
+                        const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
                         bool finite = true;
                         uint16_t *out = p.out + (w.r.t0 + tok) * p.o_t + (long long)hq * p.o_h;
-                        for (int d = 0; d < D; d += 32) {
-                            uint32_t o[32];
-                            tld32(o_tm + d, o);
+#pragma unroll 1
+                        for (int d = 0; d < D / 2; d += 16) {
+                            uint32_t o[16];
+                            tld16(o_tm + d, o);
                             float sum = 0.f;
 #pragma unroll
-                            for (int k = 0; k < 32; k += 8) {
+                            for (int k = 0; k < 16; k += 8) {
                                 float v[8];
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) {
@@ -750,7 +813,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                                     sum += fabsf(v[e]);
                                 }
                                 if (mine_row)
-                                    *reinterpret_cast<uint4 *>(out + d + k) =
+                                    *reinterpret_cast<uint4 *>(out + D / 2 * half + d + k) =
                                         make_uint4(cvt_bf2(v[0], v[1]), cvt_bf2(v[2], v[3]), cvt_bf2(v[4], v[5]), cvt_bf2(v[6], v[7]));
                             }
                             finite &= sum < INFINITY;
@@ -761,24 +824,26 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                         while (again) {
                             const int src = __ffs(again) - 1;
                             again &= again - 1;
-                            row_again<D, I8>(p, w.s, w.h, w.r.t0, w.r.n, w.r.len, __shfl_sync(0xFFFFFFFFu, r, src));
+                            // only this half's dimensions: the other half's warp sees to its own
+                            row_again<D, I8>(p, w.s, w.h, w.r.t0, w.r.n, w.r.len, __shfl_sync(0xFFFFFFFFu, r, src), D / 2 * half, D / 2 * half + D / 2);
                         }
                     } else {
                         float *dst = parts + ((size_t)(2 * cta + slot) * kPair + i * kTile + row) * LD;
-                        for (int d = 0; d < D; d += 32) {
-                            uint32_t o[32];
-                            tld32(o_tm + d, o);
+#pragma unroll 1
+                        for (int d = 0; d < D / 2; d += 16) {
+                            uint32_t o[16];
+                            tld16(o_tm + d, o);
                             if (mine_row)
 #pragma unroll
-                                for (int k = 0; k < 32; k += 4)
-                                    *reinterpret_cast<uint4 *>(dst + d + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                                for (int k = 0; k < 16; k += 4)
+                                    *reinterpret_cast<uint4 *>(dst + D / 2 * half + d + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                         }
                         fence_before();
-                        if (mine_row) *reinterpret_cast<float2 *>(dst + D) = make_float2(mx, l);
+                        if (mine_row && half == 0) *reinterpret_cast<float2 *>(dst + D) = make_float2(mx, l_all);
                         if (b0 == 0 && tid == 0) {
                             SegRec rec;
                             // the CTA that has the pair's last block
-                            rec.parts = (int)(((begin + (work - left) + w.a.nb) * nc + total - 1) / total - 1 - cta) + 1;
+                            rec.parts = (int)(((begin + (work - left) - pc.used - at + w.a.cost()) * nc + total - 1) / total - 1 - cta) + 1;
                             rec.s = w.s;
                             rec.h = w.h;
                             rec.m = w.m;
@@ -791,7 +856,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     kb += (uint32_t)(b1 - b0);
                     n += 2u * (uint32_t)(b1 - b0);
                 }
-                left -= b1 - b0;
+                if (b0 < b1) first = false;
                 w = nx;
             }
         }
@@ -816,11 +881,11 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
         if (lane == 0) atomicOr(reinterpret_cast<uint32_t *>(c.state), kDevTimeout);
         const unsigned long long d2 = global_timer() + kTimeoutNs;
         uint32_t never = 0;
-        if (warp == 8 && issued) {
+        if (warp == 16 && issued) {
             commit(&ctl->drain);
             bounded_wait(&ctl->drain, 0u, d2, &never);
         }
-        if (!I8 && warp == 9 && lane == 0)
+        if (!I8 && warp == 17 && lane == 0)
             for (int k = max(0, issued - RING); k < issued; ++k)
                 bounded_wait(&ctl->full[k % RING], (uint32_t)(k / RING) & 1u, d2, &never);
     }

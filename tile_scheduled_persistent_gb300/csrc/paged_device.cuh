@@ -20,9 +20,10 @@ __device__ __forceinline__ uint32_t cvt_bf2(float lo, float hi) {
 
 // Row r of (s, h) again, position by position with nothing but what it sees:
 // for rows whose matrix product met an infinity or NaN in a value row that only
-// other rows of the tile see (0 * inf). One warp; D / 32 dimensions a lane.
+// other rows of the tile see (0 * inf). One warp; D / 32 dimensions a lane;
+// writes dimensions [d0, d1).
 template <int D, bool I8>
-__device__ __noinline__ void row_again(const AttnParams &p, int s, int h, int t0, int n, int len, int r) {
+__device__ __noinline__ void row_again(const AttnParams &p, int s, int h, int t0, int n, int len, int r, int d0 = 0, int d1 = D) {
     constexpr int E = D / 32;
     const View &c = p.c;
     const int lane = threadIdx.x & 31, tok = r / p.G, pos = len - n + tok, hq = h * p.G + r % p.G;
@@ -62,7 +63,8 @@ __device__ __noinline__ void row_again(const AttnParams &p, int s, int h, int t0
         }
     uint16_t *out = p.out + (t0 + tok) * p.o_t + hq * p.o_h;
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[lane * E + e] = l == 0.f ? 0 : f2bf(o[e] / l);
+    for (int e = 0; e < E; ++e)
+        if (lane * E + e >= d0 && lane * E + e < d1) out[lane * E + e] = l == 0.f ? 0 : f2bf(o[e] / l);
 }
 
 }  // namespace paged
