@@ -61,20 +61,32 @@ struct TcShape {
     static constexpr int HALF = kBlock * 128;           // bytes: 128 rows of 64 BF16
     static constexpr int BLOCK = HALF * (D / 64);       // one block of K or V, or a query tile
     static constexpr int RING = D == 128 ? 4 : 8;
-    // warpgroups: four of softmax, one of the MMA issuer and the loader
-    static constexpr int THREADS = 640, LOADERS = I8 ? 96 : 32;
+    // warpgroups: four of softmax; one of the MMA issuer, the loader (INT8: two warps) and the planner
+    static constexpr int THREADS = 640, LOADERS = I8 ? 64 : 32;
     // registers a thread after the split: 4 x 104 + 64 = 5 x 96, the launch's
     static constexpr int REG_SOFTMAX = 104, REG_ISSUE = 64;
-    static constexpr int LD = D + 4;                    // floats a row of a partial state
+    static constexpr int PART = kPair * (D + 2);        // floats of a partial state: o [D / 4][row][4], m [row], l [row]
     static constexpr int SCALES = I8 ? 2 * 16 * kBlock * 4 : 0;  // bytes: a block's K and V scales, by block number
 };
 
+// What the roles need to know of a piece of work: a pair's blocks [b0, b1). b1 == 0: no more.
+struct Seg {
+    int s, h, m, t0, n, len;         // row, KV head, pair; the row's first token, tokens, length
+    int rows, b0, b1, nb;            // query rows of the pair; blocks, and how many the pair has
+    int hi, lo, head, nhb, wb0;      // positions [0, head) and [lo, hi) are seen; see PairSpan
+    int all_hi[2], all_lo[2];        // positions that every row of a tile sees
+    int slot;                        // of a partial state
+};
+constexpr int kSegRing = 4;
+
 struct Ctl {
     uint64_t full[kMaxRing], empty[kMaxRing], fix, drain, q_ready[2], s_full[2], p_full[2], o_full[2], x_ready[2][4];
+    uint64_t seg_full[kSegRing], seg_empty[kSegRing];
     uint32_t tmem, abort;
     uint32_t mask[kMaskRing];    // pages of a key block that are there, by block number
     int seg_s, seg_h, seg_m;
     long long seg_at, scan[20];
+    Seg seg[kSegRing];
     float top[4][2][2][kTile];   // row maxima of the last four blocks, of a tile's halves (the sums, at a pair's end)
 };
 
@@ -281,7 +293,7 @@ template <int D, bool I8>
 __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
     tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ TensorMap mk, const __grid_constant__ TensorMap mv) {
     using S = TcShape<D, I8>;
-    constexpr int RING = S::RING, LD = S::LD, NW = S::THREADS / 32;
+    constexpr int RING = S::RING, NW = S::THREADS / 32;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t *sq = sm;                     // two query tiles
     uint8_t *ring = sm + 2 * S::BLOCK;    // RING blocks
@@ -312,6 +324,10 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             mbar_init(&ctl->p_full[i], 256);
             for (int k = 0; k < 4; ++k) mbar_init(&ctl->x_ready[i][k], 64);
             mbar_init(&ctl->o_full[i], 1);
+        }
+        for (int i = 0; i < kSegRing; ++i) {
+            mbar_init(&ctl->seg_full[i], 1);
+            mbar_init(&ctl->seg_empty[i], 16 + 1 + S::LOADERS / 32);
         }
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -405,45 +421,105 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
     int issued = 0;
 
     if (begin < end) {
-        Walk w;
-        w.s = ctl->seg_s;
-        w.h = ctl->seg_h;
-        w.m = ctl->seg_m;
-        w.load(p);
-        // in cost units: where the piece begins in its first pair, how long it is. Of a pair that
-        // begins at unit 0, units kPairCost + b are block b.
-        const int start = (int)(begin - ctl->seg_at), work = (int)(end - begin);
-        struct Piece {
-            int b0, b1, used;
+        auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = __all_sync(0xFFFFFFFFu, bounded_wait(bar, parity & 1u, deadline, abort));
+            return ok;
         };
-        auto piece_of = [&](int at, int left) {
-            Piece r;
-            r.used = min(w.a.cost() - at, left);
-            r.b0 = max(0, at - kPairCost);
-            r.b1 = max(0, at + r.used - kPairCost);
-            return r;
+        // the k-th piece of work; false at the end (or after a timeout)
+        auto seg_begin = [&](uint32_t k) { return warp_wait(&ctl->seg_full[k % kSegRing], k / kSegRing) && ctl->seg[k % kSegRing].b1 > 0; };
+        auto seg_end = [&](uint32_t k) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->seg_empty[k % kSegRing]);
         };
-        auto block_of = [&](int b) { return b < w.a.nhb ? b : b - w.a.nhb + w.a.wb0; };
-
+        // ================================================ planner: the CTA's pieces, a few ahead of their use
+        auto planner = [&]() {
+            Walk w;
+            w.s = ctl->seg_s;
+            w.h = ctl->seg_h;
+            w.m = ctl->seg_m;
+            w.load(p);
+            uint32_t k = 0;
+            auto slot_free = [&]() { return k < kSegRing || warp_wait(&ctl->seg_empty[k % kSegRing], k / kSegRing - 1u); };
+            // in cost units: where the work begins in its first pair, how much there is. Of a pair
+            // that begins at unit 0, units kPairCost + b are block b.
+            int at = (int)(begin - ctl->seg_at), left = (int)(end - begin);
+            bool first = true;
+            while (left > 0) {
+                const int used = min(w.a.cost() - at, left), b0 = max(0, at - kPairCost), b1 = max(0, at + used - kPairCost);
+                if (b0 < b1) {
+                    if (!slot_free()) break;
+                    if (lane == 0) {
+                        Seg &g = ctl->seg[k % kSegRing];
+                        g.s = w.s;
+                        g.h = w.h;
+                        g.m = w.m;
+                        g.t0 = w.r.t0;
+                        g.n = w.r.n;
+                        g.len = w.r.len;
+                        g.rows = w.a.rows;
+                        g.b0 = b0;
+                        g.b1 = b1;
+                        g.nb = w.a.nb;
+                        g.hi = w.a.hi;
+                        g.lo = w.a.lo;
+                        g.head = w.a.head;
+                        g.nhb = w.a.nhb;
+                        g.wb0 = w.a.wb0;
+                        for (int i = 0; i < 2; ++i) {
+                            const int ra = w.m * kPair + i * kTile, rz = min(ra + kTile, w.m * kPair + w.a.rows) - 1;
+                            g.all_hi[i] = w.r.len - w.r.n + group_div(p, ra);
+                            g.all_lo[i] = p.window > 0 ? w.r.len - w.r.n + group_div(p, max(ra, rz)) - p.window + 1 : 0;
+                        }
+                        g.slot = first ? 0 : 1;
+                        if (b0 == 0 && b1 < w.a.nb) {  // others finish this pair
+                            SegRec rec;
+                            const long long pair_end = end - left - at + w.a.cost();
+                            rec.parts = (int)((pair_end * nc + total - 1) / total - 1 - cta) + 1;
+                            rec.s = w.s;
+                            rec.h = w.h;
+                            rec.m = w.m;
+                            rec.slot = g.slot;
+                            rec.pad[0] = rec.pad[1] = rec.pad[2] = 0;
+                            recs[cta] = rec;
+                        }
+                        mbar_arrive(&ctl->seg_full[k % kSegRing]);
+                    }
+                    ++k;
+                    first = false;
+                    // its queries on their way to L2
+                    for (int x = lane; x < w.a.rows; x += 32) {
+                        const int r = w.m * kPair + x, tok = group_div(p, r);
+                        const uint16_t *q = p.q + (w.r.t0 + tok) * p.q_t + (long long)(w.h * p.G + r - tok * p.G) * p.q_h;
+                        prefetch_l2(q);
+                        if (D == 128) prefetch_l2(q + 64);
+                    }
+                }
+                left -= used;
+                at = 0;
+                if (left > 0) w.next(p);
+            }
+            if (ok && slot_free() && lane == 0) {
+                ctl->seg[k % kSegRing].b1 = 0;
+                mbar_arrive(&ctl->seg_full[k % kSegRing]);
+            }
+            __syncwarp();
+        };
         // ================================================ loader
         auto loader = [&]() {
             const int lt = tid - 17 * 32;  // thread of the loader
-            int n = 0;                    // blocks of K and V so far
-            uint32_t kb = 0, fixes = 0;   // key blocks, repaired blocks so far
-            for (int at = start, left = work; left > 0 && ok; at = 0) {
-                const Piece pc = piece_of(at, left);
-                const int b0 = pc.b0, b1 = pc.b1;
-                left -= pc.used;
-                const int32_t *table = c.tables + (size_t)w.s * c.width;
-                for (int b = b0; b < b1 && ok; ++b) {
-                    const int t0 = block_of(b) * kBlock, npg = kBlock / c.ps;
+            int n = 0;                     // blocks of K and V so far
+            uint32_t kb = 0, fixes = 0;    // key blocks, repaired blocks so far
+            for (uint32_t sk = 0; seg_begin(sk); ++sk) {
+                const Seg &g = ctl->seg[sk % kSegRing];
+                const int b1 = g.b1, hi = g.hi, lo = g.lo, head = g.head, nhb = g.nhb, wb0 = g.wb0, hh = g.h;
+                const int32_t *table = c.tables + (size_t)g.s * c.width;
+                for (int b = g.b0; b < b1 && ok; ++b) {
+                    const int t0 = (b < nhb ? b : b - nhb + wb0) * kBlock, npg = kBlock >> c.psl;
                     // lane i: page i of the block, -1 where nothing of it is seen, or it is missing
                     int page = -1;
-                    bool wanted = false;
                     if (lane < npg) {
-                        const int pa = t0 + lane * c.ps, pe = pa + c.ps;
-                        wanted = pa < w.a.hi && (pe > w.a.lo || pa < w.a.head);
-                        if (wanted) {
+                        const int pa = t0 + (lane << c.psl), pe = pa + c.ps;
+                        if (pa < hi && (pe > lo || pa < head)) {
                             page = __ldg(table + (pa >> c.psl));
                             if (page < 0 || page >= c.n_pages) {
                                 page = -1;
@@ -454,34 +530,31 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     const uint32_t have = __ballot_sync(0xFFFFFFFFu, page >= 0);
                     // bits of 16 positions, for the softmax
                     uint32_t mask16 = 0;
+#pragma unroll
                     for (int i = 0; i < 8; ++i) mask16 |= ((have >> ((16 * i) >> c.psl)) & 1u) << i;
                     for (int kv = 0; kv < 2 && ok; ++kv, ++n) {
                         const int st = n % RING, round = n / RING;
-                        if (round > 0)
-                            ok = __all_sync(0xFFFFFFFFu, bounded_wait(&ctl->empty[st], (uint32_t)(round - 1) & 1u, deadline, abort));
-                        if (!ok) break;
+                        if (round > 0 && !warp_wait(&ctl->empty[st], (uint32_t)(round - 1))) break;
                         uint8_t *dst = ring + st * S::BLOCK;
                         if (kv == 0 && lt == 0) ctl->mask[kb % kMaskRing] = mask16;
                         if constexpr (!I8) {
                             // rows of V that nothing may read: zero them once the copies are in
-                            const bool repair = kv == 1 && (have != (1u << npg) - 1u ||
-                                                            t0 + kBlock > w.a.hi);
+                            const bool repair = kv == 1 && (have != (1u << npg) - 1u || t0 + kBlock > hi);
                             uint64_t *bar = repair ? &ctl->fix : &ctl->full[st];
                             if (lane == 0) mbar_expect_tx(bar, (uint32_t)(__popc(have) * c.ps * D * 2));
                             __syncwarp();
                             if (page >= 0) {
-                                const int z = page * c.nkv + w.h;
+                                const int z = page * c.nkv + hh;
 #pragma unroll
                                 for (int hf = 0; hf < D / 64; ++hf)
                                     tensor_g2s_3d(dst + hf * S::HALF + lane * c.ps * 128, kv ? &mv : &mk, 64 * hf, 0, z, bar);
                             }
                             if (repair) {
-                                ok = __all_sync(0xFFFFFFFFu, bounded_wait(&ctl->fix, fixes & 1u, deadline, abort));
-                                if (!ok) break;
+                                if (!warp_wait(&ctl->fix, fixes)) break;
                                 ++fixes;
                                 for (int i = lane; i < kBlock * (D / 8); i += 32) {
                                     const int row = i / (D / 8), u = i % (D / 8);
-                                    if (!((mask16 >> (row / 16)) & 1u) || t0 + row >= w.a.hi)
+                                    if (!((mask16 >> (row / 16)) & 1u) || t0 + row >= hi)
                                         *reinterpret_cast<uint4 *>(dst + (u / 8) * S::HALF + row * 128 + (((u % 8) ^ (row & 7)) << 4)) =
                                             make_uint4(0u, 0u, 0u, 0u);
                                 }
@@ -493,32 +566,31 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                             // 16 codes a step: a row is D / 16 steps
                             const uint8_t *pool = kv ? c.v : c.k;
                             const float *scales = kv ? c.vs : c.ks;
-                            constexpr int UPR = D / 16, UNITS = kBlock * UPR;
-                            constexpr int STEPS = (UNITS + S::LOADERS - 1) / S::LOADERS, AT_ONCE = 4;
-                            for (int r = lt; r < kBlock + S::LOADERS; r += S::LOADERS) {
-                                const int pg = __shfl_sync(0xFFFFFFFFu, page, (r & (kBlock - 1)) >> c.psl);
-                                if (r >= kBlock) break;
+                            constexpr int UPR = D / 16, STEPS = kBlock * UPR / S::LOADERS, AT_ONCE = 4;
+                            static_assert(STEPS % AT_ONCE == 0, "whole groups of loads");
+#pragma unroll
+                            for (int r = lt; r < kBlock; r += S::LOADERS) {
+                                const int pg = __shfl_sync(0xFFFFFFFFu, page, r >> c.psl);
                                 float f = 0.f;
-                                if (pg >= 0 && t0 + r < w.a.hi)
-                                    f = __ldg(scales + ((size_t)pg * c.nkv + w.h) * c.ps + (r & (c.ps - 1)));
+                                if (pg >= 0 && t0 + r < hi)
+                                    f = __ldg(scales + ((size_t)pg * c.nkv + hh) * c.ps + (r & (c.ps - 1)));
                                 scale[kv][kb % kMaskRing][r] = f;
                             }
-                            __syncwarp();
+#pragma unroll 1
                             for (int k0 = 0; k0 < STEPS; k0 += AT_ONCE) {
                                 uint4 w4[AT_ONCE];
 #pragma unroll
                                 for (int k = 0; k < AT_ONCE; ++k) {
-                                    const int i = lt + S::LOADERS * (k0 + k), row = (i / UPR) & (kBlock - 1), u = i % UPR;
+                                    const int i = lt + S::LOADERS * (k0 + k), row = i / UPR, u = i % UPR;
                                     const int pg = __shfl_sync(0xFFFFFFFFu, page, row >> c.psl);
                                     w4[k] = make_uint4(0u, 0u, 0u, 0u);
-                                    if (i < UNITS && pg >= 0 && (kv == 0 || t0 + row < w.a.hi))
+                                    if (pg >= 0 && (kv == 0 || t0 + row < hi))
                                         w4[k] = __ldg(reinterpret_cast<const uint4 *>(
-                                            pool + (((size_t)pg * c.nkv + w.h) * c.ps + (row & (c.ps - 1))) * D + 16 * u));
+                                            pool + (((size_t)pg * c.nkv + hh) * c.ps + (row & (c.ps - 1))) * D + 16 * u));
                                 }
 #pragma unroll
                                 for (int k = 0; k < AT_ONCE; ++k) {
                                     const int i = lt + S::LOADERS * (k0 + k), row = i / UPR, u = i % UPR;
-                                    if (i >= UNITS) break;
                                     const uint32_t x[4] = {w4[k].x, w4[k].y, w4[k].z, w4[k].w};
                                     uint32_t y[8];
 #pragma unroll
@@ -537,7 +609,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     }
                     ++kb;
                 }
-                if (left > 0) w.next(p);
+                seg_end(sk);
             }
             issued = n;
         };
@@ -548,7 +620,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             int n = 0;
             uint32_t seg[2] = {0, 0}, step[2] = {0, 0};
             auto wait = [&](uint64_t *bar, uint32_t parity) {
-                ok = __all_sync(0xFFFFFFFFu, bounded_wait(bar, parity & 1u, deadline, abort));
+                warp_wait(bar, parity);
                 fence_after();
                 return ok;
             };
@@ -561,17 +633,12 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                 }
                 commit(&ctl->s_full[i]);
             };
-            for (int at = start, left = work; left > 0 && ok; at = 0) {
-                const Piece pc = piece_of(at, left);
-                const int b0 = pc.b0, b1 = pc.b1;
-                left -= pc.used;
-                const int nt = w.a.rows > kTile ? 2 : 1;
-                if (b0 >= b1) {  // only the pair's first cost units: the next CTA begins it
-                    if (left > 0) w.next(p);
-                    continue;
-                }
+            for (uint32_t sg = 0; seg_begin(sg); ++sg) {
+                const int nt = ctl->seg[sg % kSegRing].rows > kTile ? 2 : 1;
+                int left = ctl->seg[sg % kSegRing].b1 - ctl->seg[sg % kSegRing].b0;
+                uint32_t acc = 0;
                 if (!wait(&ctl->full[n % RING], (uint32_t)(n / RING))) break;
-                for (int i = 0; i < nt && ok; ++i) {
+                for (int i = 0; i < nt; ++i) {
                     if (!wait(&ctl->q_ready[i], seg[i])) break;
                     ++seg[i];
                     issued = 1;
@@ -579,27 +646,31 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                 }
                 if (!ok) break;
                 commit(&ctl->empty[n % RING]);
-                for (int b = b0; b < b1 && ok; ++b, n += 2) {
+                for (; left > 0; --left, n += 2, acc = 1) {
                     const int sv = (n + 1) % RING, sk = (n + 2) % RING;
+                    // what the tensor cores need besides the weights is there long before them
                     if (!wait(&ctl->full[sv], (uint32_t)((n + 1) / RING))) break;
+                    if (left > 1 && !wait(&ctl->full[sk], (uint32_t)((n + 2) / RING))) break;
                     const uint64_t bv = desc_mn(smem_u32(ring + sv * S::BLOCK), S::HALF);
-                    for (int i = 0; i < nt && ok; ++i) {
+                    for (int i = 0; i < nt; ++i) {
                         if (!wait(&ctl->p_full[i], step[i])) break;
+                        ++step[i];
 #pragma unroll
                         for (int k = 0; k < kBlock / 16; ++k)
-                            mma_ts(o_tm + D * i, tmem + 128 * i + 64 * (k / 4) + 8 * (k % 4), bv + (uint64_t)(k * (2048 >> 4)), id_o, b > b0 || k > 0);
-                        ++step[i];
+                            mma_ts(o_tm + D * i, tmem + 128 * i + 64 * (k / 4) + 8 * (k % 4), bv + (uint64_t)(k * (2048 >> 4)), id_o,
+                                   k > 0 ? 1u : acc);
                         if (i == nt - 1) commit(&ctl->empty[sv]);
-                        if (b + 1 < b1) {
-                            if (i == 0 && !wait(&ctl->full[sk], (uint32_t)((n + 2) / RING))) break;
+                        if (left > 1) {
                             s_mma(i, sk);
                             if (i == nt - 1) commit(&ctl->empty[sk]);
                         } else {
                             commit(&ctl->o_full[i]);
                         }
                     }
+                    if (!ok) break;
                 }
-                if (left > 0) w.next(p);
+                if (!ok) break;
+                seg_end(sg);
             }
         };
         // ================================================ softmax, half a query row a thread
@@ -607,10 +678,13 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             regs_down<S::REG_ISSUE>();
             if (warp == 16)
                 issuer();
+            else if (warp == 19)
+                planner();
             else if (I8 || warp == 17)
                 loader();
         } else {
             regs_up<S::REG_SOFTMAX>();
+            constexpr int U = D / 16;  // 16-byte units of half a row
             const int i = warp >> 3, half = (warp >> 2) & 1, row = tid & 127;
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
             // this thread's scores, and its weights in place of them (not of the other half's, whose
@@ -623,241 +697,216 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             auto exchange = [&](uint32_t block, float v) {
                 top_of(block, half) = v;
                 mbar_arrive(x_ready);
-                ok = __all_sync(0xFFFFFFFFu, bounded_wait(x_ready, xs & 1u, deadline, abort));
+                warp_wait(x_ready, xs);
                 ++xs;
                 return top_of(block, half ^ 1);
             };
-            uint32_t step = 0, seg = 0, kb = 0;
-            bool first = true;  // no pair with blocks so far
-            uint32_t n = 0;  // ring blocks before the current key block
-            for (int at = start, left = work; left > 0 && ok; at = 0) {
-                const Piece pc = piece_of(at, left);
-                const int b0 = pc.b0, b1 = pc.b1;
-                left -= pc.used;
-                const int r = w.m * kPair + i * kTile + row;     // of the (sequence, KV head)
-                const bool mine_row = i * kTile + row < w.a.rows;
-                const bool tile_on = i * kTile < w.a.rows && b0 < b1;
-                const int tok = group_div(p, r), hq = w.h * p.G + r - tok * p.G;
-                const int lim = mine_row ? w.r.len - w.r.n + tok : -1;
-                if (tile_on) {
-                    const uint16_t *q = p.q + (w.r.t0 + tok) * p.q_t + (long long)hq * p.q_h;
-                    uint8_t *dst = sq + i * S::BLOCK + row * 128;
+            // unit u of this half of tile row r in shared memory (queries, and the output on its way)
+            auto staged = [&](int r, int u) {
+                const int x = half * U + u;
+                return reinterpret_cast<uint4 *>(sq + i * S::BLOCK + (x / 8) * S::HALF + r * 128 + (((x % 8) ^ (r & 7)) << 4));
+            };
+            uint32_t step = 0, tseg = 0, kb = 0, n = 0;  // n: ring blocks before the current key block
+            for (uint32_t sg = 0; seg_begin(sg); ++sg) {
+                const Seg &g = ctl->seg[sg % kSegRing];
+                const int r0 = g.m * kPair + i * kTile;  // the tile's first query row
+                const int rows = min(kTile, g.rows - i * kTile);
+                const int b0 = g.b0, b1 = g.b1;
+                if (rows <= 0) {
+                    kb += (uint32_t)(b1 - b0);
+                    n += 2u * (uint32_t)(b1 - b0);
+                    seg_end(sg);
+                    continue;
+                }
+                // element offset of a tile row in q or out
+                auto offset = [&](int r, long long st, long long sh) {
+                    const int tok = group_div(p, r0 + r);
+                    return (g.t0 + tok) * st + (long long)(g.h * p.G + r0 + r - tok * p.G) * sh;
+                };
+                // queries: U lanes a row, so that a warp reads whole 64- or 128-byte runs
+                {
+                    uint4 x[U];
 #pragma unroll
-                    for (int v = 0; v < D / 16; ++v) {
-                        const int u = D / 16 * half + v;
-                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                        if (mine_row) x = __ldg(reinterpret_cast<const uint4 *>(q + 8 * u));
-                        *reinterpret_cast<uint4 *>(dst + (u / 8) * S::HALF + (((u % 8) ^ (row & 7)) << 4)) = x;
+                    for (int v = 0; v < U; ++v) {
+                        const int r = 32 * (warp & 3) + v * (32 / U) + lane / U;
+                        x[v] = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < rows)
+                            x[v] = __ldg(reinterpret_cast<const uint4 *>(p.q + offset(r, p.q_t, p.q_h) + 8 * (half * U + lane % U)));
                     }
+#pragma unroll
+                    for (int v = 0; v < U; ++v) *staged(32 * (warp & 3) + v * (32 / U) + lane / U, lane % U) = x[v];
                     fence_proxy_async_smem();
                     mbar_arrive(&ctl->q_ready[i]);
                 }
+                const int lim = row < rows ? g.len - g.n + group_div(p, r0 + row) : -1;
+                const int all_hi = g.all_hi[i], all_lo = g.all_lo[i];
                 // rows that see nothing need no maximum
                 float mx = lim < 0 ? 0.f : -INFINITY, l = 0.f, top1 = -INFINITY, top2 = -INFINITY;
-                if (tile_on) {
-                    // positions every row of the tile sees
-                    const int ra = w.m * kPair + i * kTile, rz = min(ra + kTile, w.m * kPair + w.a.rows) - 1;
-                    const int all_hi = w.r.len - w.r.n + group_div(p, ra);
-                    const int all_lo = p.window > 0 ? w.r.len - w.r.n + group_div(p, rz) - p.window + 1 : 0;
-                    for (int b = b0; b < b1; ++b, ++kb, n += 2) {
-                        ok = bounded_wait(&ctl->s_full[i], step & 1u, deadline, abort);
-                        ok = __all_sync(0xFFFFFFFFu, ok);
-                        if (!ok) break;
-                        ++step;
-                        fence_after();
-                        const int t0 = block_of(b) * kBlock + 64 * half;  // of this thread's positions
-                        const uint32_t mask = ctl->mask[kb % kMaskRing] >> (4 * half);
-                        uint32_t x[64];
-                        tld64(s_tm, x);
-                        if constexpr (I8) {
-                            const float4 *ks = reinterpret_cast<const float4 *>(scale[0][kb % kMaskRing] + 64 * half);
+                for (int b = b0; b < b1; ++b, ++kb, n += 2) {
+                    if (!warp_wait(&ctl->s_full[i], step)) break;
+                    ++step;
+                    fence_after();
+                    // written before the other half's weights of the last block, so visible now
+                    const float other2 = b - b0 >= 2 ? top_of(kb + 2, half ^ 1) : -INFINITY;
+                    const int t0 = (b < g.nhb ? b : b - g.nhb + g.wb0) * kBlock + 64 * half;  // of this thread's positions
+                    const uint32_t mask = ctl->mask[kb % kMaskRing] >> (4 * half);
+                    uint32_t x[64];
+                    tld64(s_tm, x);
+                    if constexpr (I8) {
+                        const float4 *ks = reinterpret_cast<const float4 *>(scale[0][kb % kMaskRing] + 64 * half);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float4 f = ks[j];
-                                x[4 * j] = __float_as_uint(__uint_as_float(x[4 * j]) * f.x);
-                                x[4 * j + 1] = __float_as_uint(__uint_as_float(x[4 * j + 1]) * f.y);
-                                x[4 * j + 2] = __float_as_uint(__uint_as_float(x[4 * j + 2]) * f.z);
-                                x[4 * j + 3] = __float_as_uint(__uint_as_float(x[4 * j + 3]) * f.w);
-                            }
+                        for (int j = 0; j < 16; ++j) {
+                            const float4 f = ks[j];
+                            x[4 * j] = __float_as_uint(__uint_as_float(x[4 * j]) * f.x);
+                            x[4 * j + 1] = __float_as_uint(__uint_as_float(x[4 * j + 1]) * f.y);
+                            x[4 * j + 2] = __float_as_uint(__uint_as_float(x[4 * j + 2]) * f.z);
+                            x[4 * j + 3] = __float_as_uint(__uint_as_float(x[4 * j + 3]) * f.w);
                         }
-                        if ((mask & 0xFu) != 0xFu || t0 + 63 > all_hi || t0 < all_lo) {
-                            // a bit per position (what is seen is a range of the row and the sinks)
+                    }
+                    if ((mask & 0xFu) != 0xFu || t0 + 63 > all_hi || t0 < all_lo) {
+                        // a bit per position (what is seen is a range of the row and the sinks)
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const int tb = t0 + 32 * k;
-                                uint32_t see = low_bits(lim + 1 - tb);
-                                if (p.window > 0)
-                                    see &= ~low_bits(lim - p.window + 1 - tb) | low_bits(p.sinks - tb);
-                                see &= ((mask >> (2 * k)) & 1u ? 0xFFFFu : 0u) | ((mask >> (2 * k + 1)) & 1u ? 0xFFFF0000u : 0u);
+                        for (int k = 0; k < 2; ++k) {
+                            const int tb = t0 + 32 * k;
+                            uint32_t see = low_bits(lim + 1 - tb);
+                            if (p.window > 0) see &= ~low_bits(lim - p.window + 1 - tb) | low_bits(p.sinks - tb);
+                            see &= ((mask >> (2 * k)) & 1u ? 0xFFFFu : 0u) | ((mask >> (2 * k + 1)) & 1u ? 0xFFFF0000u : 0u);
 #pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    if (!((see >> j) & 1u)) x[32 * k + j] = 0xFF800000u;
-                            }
+                            for (int j = 0; j < 32; ++j)
+                                if (!((see >> j) & 1u)) x[32 * k + j] = 0xFF800000u;
                         }
-                        auto block_top = [&]() {
-                            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    }
+                    auto block_top = [&]() {
+                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                            for (int j = 0; j < 64; j += 8)
+                        for (int j = 0; j < 64; j += 8)
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    m4[k] = max3(m4[k], __uint_as_float(x[j + k]), __uint_as_float(x[j + 4 + k]));
-                            return max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * p.scale_log2;
-                        };
-                        // the row's reference: what both halves had seen two blocks ago
-                        float nm = mx;
-                        if (b - b0 >= 2) {
-                            const float t = fmaxf(top2, top_of(kb + 2, half ^ 1));
-                            if (t > mx + kRise) nm = t;
-                        }
+                            for (int k = 0; k < 4; ++k)
+                                m4[k] = max3(m4[k], __uint_as_float(x[j + k]), __uint_as_float(x[j + 4 + k]));
+                        return max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * p.scale_log2;
+                    };
+                    // the row's reference: what both halves had seen two blocks ago
+                    const float seen = fmaxf(top2, other2);
+                    if (__any_sync(0xFFFFFFFFu, mx == -INFINITY || seen > mx + kRise)) {
+                        float nm = seen > mx + kRise ? seen : mx;
                         if (__any_sync(0xFFFFFFFFu, mx == -INFINITY)) {  // rows that have seen nothing yet
                             const float t = block_top(), u = fmaxf(t, exchange(kb, t));
                             if (!ok) break;
                             if (mx == -INFINITY) nm = u;
                         }
-                        if (__any_sync(0xFFFFFFFFu, nm > mx)) {
-                            const float corr = nm > mx ? ex2(mx - nm) : 1.f;
-                            mx = nm;
-                            l *= corr;
-                            if (b > b0) {
-                                // the last P V is complete: it was issued before this block's S
+                        const float corr = nm > mx ? ex2(mx - nm) : 1.f;
+                        mx = nm;
+                        l *= corr;
+                        if (b > b0) {
+                            // the last P V is complete: it was issued before this block's S
 #pragma unroll 1
-                                for (int d = 0; d < D / 2; d += 16) {
-                                    uint32_t o[16];
-                                    tld16(o_tm + d, o);
+                            for (int d = 0; d < D / 2; d += 16) {
+                                uint32_t o[16];
+                                tld16(o_tm + d, o);
 #pragma unroll
-                                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
-                                    tst16(o_tm + d, o);
-                                }
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+                                tst16(o_tm + d, o);
                             }
                         }
-                        const float base = mx == -INFINITY ? 0.f : mx;
-                        const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2), nb2 = pack2(-base, -base);
-                        uint64_t ls[2] = {0ull, 0ull};  // sums of even and odd positions, two chains
-                        const float *vs = nullptr;
-                        if constexpr (I8) {
-                            // the value block's scales: its copy is in once the block after the keys is full
-                            ok = __all_sync(0xFFFFFFFFu, bounded_wait(&ctl->full[(n + 1) % RING], ((n + 1) / RING) & 1u, deadline, abort));
-                            if (!ok) break;
-                            vs = scale[1][kb % kMaskRing] + 64 * half;
-                        }
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const int k = q * 32 + 2 * j;
-                                float e0, e1;
-                                unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), sc2, nb2), e0, e1);
-                                e0 = ex2(e0);
-                                e1 = ex2(e1);
-                                ls[j & 1] = add2(ls[j & 1], pack2(e0, e1));
-                                if constexpr (I8) {
-                                    const float2 f = *reinterpret_cast<const float2 *>(vs + k);
-                                    e0 *= f.x;
-                                    e1 *= f.y;
-                                }
-                                pk[j] = cvt_bf2(e0, e1);
-                            }
-                            tst16(p_tm + 16 * q, pk);
-                        }
-                        tst_wait();
-                        fence_before();
-                        mbar_arrive(&ctl->p_full[i]);
-                        // off the path to the next product
-                        float l0, l1;
-                        unpack2(add2(ls[0], ls[1]), l0, l1);
-                        l += l0 + l1;
-                        top2 = top1;
-                        top1 = block_top();
-                        top_of(kb, half) = top1;
                     }
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                }
-                // the next pair, while the last product runs
-                Walk nx = w;
-                if (ok && left > 0) {
-                    nx.next(p);
-                    const int nr = nx.m * kPair + i * kTile + row, nt = group_div(p, nr);
-                    if (i * kTile + row < nx.a.rows) {
-                        const uint16_t *q = p.q + (nx.r.t0 + nt) * p.q_t + (long long)(nx.h * p.G + nr - nt * p.G) * p.q_h;
-                        prefetch_l2(q);
-                        if (D == 128) prefetch_l2(q + 64);
+                    const float base = mx == -INFINITY ? 0.f : mx;
+                    const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2), nb2 = pack2(-base, -base);
+                    uint64_t ls[2] = {0ull, 0ull};  // sums of even and odd positions, two chains
+                    const float *vs = nullptr;
+                    if constexpr (I8) {
+                        // the value block's scales: its copy is in once the block after the keys is full
+                        if (!warp_wait(&ctl->full[(n + 1) % RING], (n + 1) / RING)) break;
+                        vs = scale[1][kb % kMaskRing] + 64 * half;
                     }
-                }
-                if (tile_on) {
-                    // ---- the pair's output, or this piece's state
-                    ok = ok && bounded_wait(&ctl->o_full[i], seg & 1u, deadline, abort);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok) break;
-                    ++seg;
-                    fence_after();
-                    const float l_all = l + exchange(kb, l);
-                    if (!ok) break;
-                    const bool whole = b0 == 0 && b1 == w.a.nb;
-                    const int slot = first ? 0 : 1;
-                    if (whole) {
-                        const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
-                        bool finite = true;
-                        uint16_t *out = p.out + (w.r.t0 + tok) * p.o_t + (long long)hq * p.o_h;
-#pragma unroll 1
-                        for (int d = 0; d < D / 2; d += 16) {
-                            uint32_t o[16];
-                            tld16(o_tm + d, o);
-                            float sum = 0.f;
 #pragma unroll
-                            for (int k = 0; k < 16; k += 8) {
-                                float v[8];
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t pk[16];
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    v[e] = __uint_as_float(o[k + e]) * inv;
-                                    sum += fabsf(v[e]);
-                                }
-                                if (mine_row)
-                                    *reinterpret_cast<uint4 *>(out + D / 2 * half + d + k) =
-                                        make_uint4(cvt_bf2(v[0], v[1]), cvt_bf2(v[2], v[3]), cvt_bf2(v[4], v[5]), cvt_bf2(v[6], v[7]));
+                        for (int j = 0; j < 16; ++j) {
+                            const int k = q * 32 + 2 * j;
+                            float e0, e1;
+                            unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), sc2, nb2), e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            ls[j & 1] = add2(ls[j & 1], pack2(e0, e1));
+                            if constexpr (I8) {
+                                const float2 f = *reinterpret_cast<const float2 *>(vs + k);
+                                e0 *= f.x;
+                                e1 *= f.y;
                             }
-                            finite &= sum < INFINITY;
+                            pk[j] = cvt_bf2(e0, e1);
                         }
-                        fence_before();
-                        __syncwarp();
-                        uint32_t again = __ballot_sync(0xFFFFFFFFu, mine_row && !finite && w.r.n > 1);
-                        while (again) {
-                            const int src = __ffs(again) - 1;
-                            again &= again - 1;
-                            // only this half's dimensions: the other half's warp sees to its own
-                            row_again<D, I8>(p, w.s, w.h, w.r.t0, w.r.n, w.r.len, __shfl_sync(0xFFFFFFFFu, r, src), D / 2 * half, D / 2 * half + D / 2);
-                        }
-                    } else {
-                        float *dst = parts + ((size_t)(2 * cta + slot) * kPair + i * kTile + row) * LD;
+                        tst16(p_tm + 16 * q, pk);
+                    }
+                    tst_wait();
+                    fence_before();
+                    mbar_arrive(&ctl->p_full[i]);
+                    // off the path to the next product
+                    float l0, l1;
+                    unpack2(add2(ls[0], ls[1]), l0, l1);
+                    l += l0 + l1;
+                    top2 = top1;
+                    top1 = block_top();
+                    top_of(kb, half) = top1;
+                }
+                // ---- the pair's output, or this piece's state
+                if (!ok || !warp_wait(&ctl->o_full[i], tseg)) break;
+                ++tseg;
+                fence_after();
+                l += exchange(kb, l);
+                if (!ok) break;
+                if (b0 == 0 && b1 == g.nb) {
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    float sum = 0.f;
 #pragma unroll 1
-                        for (int d = 0; d < D / 2; d += 16) {
-                            uint32_t o[16];
-                            tld16(o_tm + d, o);
-                            if (mine_row)
+                    for (int d = 0; d < D / 2; d += 16) {
+                        uint32_t o[16];
+                        tld16(o_tm + d, o);
+                        float v[16];
 #pragma unroll
-                                for (int k = 0; k < 16; k += 4)
-                                    *reinterpret_cast<uint4 *>(dst + D / 2 * half + d + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        for (int k = 0; k < 16; ++k) {
+                            v[k] = __uint_as_float(o[k]) * inv;
+                            sum += fabsf(v[k]);
                         }
-                        fence_before();
-                        if (mine_row && half == 0) *reinterpret_cast<float2 *>(dst + D) = make_float2(mx, l_all);
-                        if (b0 == 0 && tid == 0) {
-                            SegRec rec;
-                            // the CTA that has the pair's last block
-                            rec.parts = (int)(((begin + (work - left) - pc.used - at + w.a.cost()) * nc + total - 1) / total - 1 - cta) + 1;
-                            rec.s = w.s;
-                            rec.h = w.h;
-                            rec.m = w.m;
-                            rec.slot = slot;
-                            rec.pad[0] = rec.pad[1] = rec.pad[2] = 0;
-                            recs[cta] = rec;
-                        }
+                        *staged(row, d / 8) = make_uint4(cvt_bf2(v[0], v[1]), cvt_bf2(v[2], v[3]), cvt_bf2(v[4], v[5]), cvt_bf2(v[6], v[7]));
+                        *staged(row, d / 8 + 1) =
+                            make_uint4(cvt_bf2(v[8], v[9]), cvt_bf2(v[10], v[11]), cvt_bf2(v[12], v[13]), cvt_bf2(v[14], v[15]));
+                    }
+                    fence_before();
+                    __syncwarp();
+#pragma unroll
+                    for (int v = 0; v < U; ++v) {
+                        const int r = 32 * (warp & 3) + v * (32 / U) + lane / U;
+                        if (r < rows)
+                            *reinterpret_cast<uint4 *>(p.out + offset(r, p.o_t, p.o_h) + 8 * (half * U + lane % U)) = *staged(r, lane % U);
+                    }
+                    __syncwarp();
+                    uint32_t again = __ballot_sync(0xFFFFFFFFu, row < rows && !(sum < INFINITY) && g.n > 1);
+                    while (again) {
+                        const int src = __ffs(again) - 1;
+                        again &= again - 1;
+                        // only this half's dimensions: the other half's warp sees to its own
+                        row_again<D, I8>(p, g.s, g.h, g.t0, g.n, g.len, r0 + 32 * (warp & 3) + src, D / 2 * half, D / 2 * half + D / 2);
                     }
                 } else {
-                    kb += (uint32_t)(b1 - b0);
-                    n += 2u * (uint32_t)(b1 - b0);
+                    float *dst = parts + (size_t)(2 * cta + g.slot) * S::PART;
+                    const int pr = i * kTile + row;
+#pragma unroll 1
+                    for (int d = 0; d < D / 2; d += 16) {
+                        uint32_t o[16];
+                        tld16(o_tm + d, o);
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4)
+                            *reinterpret_cast<uint4 *>(dst + (size_t)((D / 2 * half + d + k) / 4 * kPair + pr) * 4) =
+                                make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                    }
+                    fence_before();
+                    if (half == 0) {
+                        dst[D * kPair + pr] = mx;
+                        dst[(D + 1) * kPair + pr] = l;
+                    }
                 }
-                if (b0 < b1) first = false;
-                w = nx;
+                seg_end(sg);
             }
         }
     }
@@ -897,56 +946,74 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
     }
 }
 
-// Adds up the states of the pair that CTA blockIdx.x began; a warp per query row.
+// Adds up the states of the pair that CTA blockIdx.x began, 32 of its query rows a
+// block: a row a lane and 4 dimensions a warp and step, as the states are laid out;
+// the output goes through shared memory, so that rows are written in whole lines.
 template <int D, bool I8>
 __global__ void __launch_bounds__(256) tc_join_kernel(const __grid_constant__ AttnParams p) {
     using S = TcShape<D, I8>;
-    constexpr int LD = S::LD, E = D / 32;
-    const int lane = threadIdx.x & 31, cta = blockIdx.x, q = blockIdx.y * 8 + (threadIdx.x >> 5);
+    constexpr int E = D / 32;
+    __shared__ __align__(16) uint16_t so[32][D + 8];
+    __shared__ int again[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x, q0 = blockIdx.y * 32;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const SegRec rec = reinterpret_cast<const SegRec *>(p.ws)[cta];
     if (rec.parts == 0) return;
     bool bad = false;
     const RowSpan r = row_span(p, rec.s, &bad);
-    const int row = rec.m * kPair + q;
-    if (row >= r.n * p.G) return;
-    const float *parts = p.ws + (size_t)p.ctas * (sizeof(SegRec) / 4) + (size_t)q * LD;
-    auto part = [&](int i) { return parts + (size_t)(2 * (cta + i) + (i == 0 ? rec.slot : 0)) * kPair * LD; };
-    float M = -INFINITY;
-    for (int i = lane; i < rec.parts; i += 32) M = fmaxf(M, __ldcg(part(i) + D));
-    M = warp_max(M);
-    const float base = M == -INFINITY ? 0.f : M;
-    float o[E], l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    const int rows = min(32, r.n * p.G - rec.m * kPair - q0);  // of this block
+    if (rows <= 0) return;
+    if (warp == 0) again[lane] = 0;
+    __syncthreads();
+    const float *parts = p.ws + (size_t)p.ctas * (sizeof(SegRec) / 4);
+    auto part = [&](int i) { return parts + (size_t)(2 * (cta + i) + (i == 0 ? rec.slot : 0)) * S::PART; };
+    const int q = q0 + lane;
+    if (lane < rows) {
+        float M = -INFINITY;
 #pragma unroll 4
-    for (int i = 0; i < rec.parts; ++i) {
-        const float *a = part(i);
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a + D));
-        const float f = ex2(ml.x - base);
-        l = fmaf(f, ml.y, l);
-        float v[E];
-        if constexpr (E == 4)
-            *reinterpret_cast<float4 *>(v) = __ldcg(reinterpret_cast<const float4 *>(a + 4 * lane));
-        else
-            *reinterpret_cast<float2 *>(v) = __ldcg(reinterpret_cast<const float2 *>(a + 2 * lane));
+        for (int i = 0; i < rec.parts; ++i) M = fmaxf(M, __ldcg(part(i) + D * kPair + q));
+        const float base = M == -INFINITY ? 0.f : M;
+        float4 o[E];
+        float l = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(f, v[e], o[e]);
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t *out = p.out + (r.t0 + row / p.G) * p.o_t + (long long)(rec.h * p.G + row % p.G) * p.o_h + E * lane;
-    float sum = l;
+        for (int e = 0; e < E; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int i = 0; i < rec.parts; ++i) {
+            const float *a = part(i);
+            const float f = ex2(__ldcg(a + D * kPair + q) - base);
+            l = fmaf(f, __ldcg(a + (D + 1) * kPair + q), l);
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-        *reinterpret_cast<uint32_t *>(out + e) = cvt_bf2(o[e] * inv, o[e + 1] * inv);
-        sum += fabsf(o[e]) + fabsf(o[e + 1]);
+            for (int e = 0; e < E; ++e) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(a) + (size_t)(warp + 8 * e) * kPair + q);
+                o[e].x = fmaf(f, v.x, o[e].x);
+                o[e].y = fmaf(f, v.y, o[e].y);
+                o[e].z = fmaf(f, v.z, o[e].z);
+                o[e].w = fmaf(f, v.w, o[e].w);
+            }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        float sum = l;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            sum += fabsf(o[e].x) + fabsf(o[e].y) + fabsf(o[e].z) + fabsf(o[e].w);
+            *reinterpret_cast<uint2 *>(&so[lane][4 * (warp + 8 * e)]) =
+                make_uint2(cvt_bf2(o[e].x * inv, o[e].y * inv), cvt_bf2(o[e].z * inv, o[e].w * inv));
+        }
+        if (r.n > 1 && !(sum < INFINITY)) again[lane] = 1;
     }
-    __syncwarp();
-    if (r.n > 1 && __any_sync(0xFFFFFFFFu, !(sum < INFINITY))) row_again<D, I8>(p, rec.s, rec.h, r.t0, r.n, r.len, row);
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * (D / 8); i += 256) {
+        const int row = i / (D / 8), u = i % (D / 8), x = rec.m * kPair + q0 + row, tok = group_div(p, x);
+        *reinterpret_cast<uint4 *>(p.out + (r.t0 + tok) * p.o_t + (long long)(rec.h * p.G + x - tok * p.G) * p.o_h + 8 * u) =
+            *reinterpret_cast<const uint4 *>(&so[row][8 * u]);
+    }
+    __syncthreads();
+    for (int row = warp; row < rows; row += 8)
+        if (again[row]) row_again<D, I8>(p, rec.s, rec.h, r.t0, r.n, r.len, rec.m * kPair + q0 + row);
 }
 
 // ------------------------------------------------------------------ host side
-size_t tc_ws_bytes(int sms, int d) { return (size_t)sms * (sizeof(SegRec) + (size_t)2 * kPair * (d + 4) * 4); }
+size_t tc_ws_bytes(int sms, int d) { return (size_t)sms * (sizeof(SegRec) + (size_t)2 * kPair * (d + 2) * 4); }
 
 template <int D, bool I8>
 static cudaError_t launch(const AttnParams &p, cudaStream_t st) {
@@ -971,7 +1038,7 @@ static cudaError_t launch(const AttnParams &p, cudaStream_t st) {
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)p.ctas, kPair / 8);
+    cfg.gridDim = dim3((unsigned)p.ctas, kPair / 32);
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cfg.attrs = at;
