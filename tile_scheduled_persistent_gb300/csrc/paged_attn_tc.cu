@@ -65,6 +65,10 @@ struct TcShape {
     static constexpr int THREADS = 640, LOADERS = I8 ? 64 : 32;
     // registers a thread after the split: 4 x 104 + 64 = 5 x 96, the launch's
     static constexpr int REG_SOFTMAX = 104, REG_ISSUE = 64;
+    // tensor memory, 512 columns: scores of the two tiles (128 each), O (D each) and, at D 64,
+    // room for the weights of their own; at D 128 they take the place of the scores
+    static constexpr bool SPLIT = D == 64;
+    static constexpr int O_COL = 256, P_COL = SPLIT ? 384 : 0, P_TILE = SPLIT ? 64 : 128, P_HALF = SPLIT ? 32 : 64;
     static constexpr int PART = kPair * (D + 2);        // floats of a partial state: o [D / 4][row][4], m [row], l [row]
     static constexpr int SCALES = I8 ? 2 * 16 * kBlock * 4 : 0;  // bytes: a block's K and V scales, by block number
 };
@@ -76,11 +80,12 @@ struct Seg {
     int hi, lo, head, nhb, wb0;      // positions [0, head) and [lo, hi) are seen; see PairSpan
     int all_hi[2], all_lo[2];        // positions that every row of a tile sees
     int slot;                        // of a partial state
+    uint32_t q_at[kPair], o_at[kPair];  // where the query rows lie in q and out, in 16-byte units
 };
-constexpr int kSegRing = 4;
+constexpr int kSegRing = 3;
 
 struct Ctl {
-    uint64_t full[kMaxRing], empty[kMaxRing], fix, drain, q_ready[2], s_full[2], p_full[2], o_full[2], x_ready[2][4];
+    uint64_t full[kMaxRing], empty[kMaxRing], fix, drain, q_ready[2], s_full[2], s_free[2], p_full[2], o_done[2], x_ready[2][4];
     uint64_t seg_full[kSegRing], seg_empty[kSegRing];
     uint32_t tmem, abort;
     uint32_t mask[kMaskRing];    // pages of a key block that are there, by block number
@@ -323,7 +328,8 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             mbar_init(&ctl->s_full[i], 1);
             mbar_init(&ctl->p_full[i], 256);
             for (int k = 0; k < 4; ++k) mbar_init(&ctl->x_ready[i][k], 64);
-            mbar_init(&ctl->o_full[i], 1);
+            mbar_init(&ctl->s_free[i], 256);
+            mbar_init(&ctl->o_done[i], 1);
         }
         for (int i = 0; i < kSegRing; ++i) {
             mbar_init(&ctl->seg_full[i], 1);
@@ -427,6 +433,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
         };
         // the k-th piece of work; false at the end (or after a timeout)
         auto seg_begin = [&](uint32_t k) { return warp_wait(&ctl->seg_full[k % kSegRing], k / kSegRing) && ctl->seg[k % kSegRing].b1 > 0; };
+        auto seg_peek = [&](uint32_t k) { return warp_wait(&ctl->seg_full[k % kSegRing], k / kSegRing); };
         auto seg_end = [&](uint32_t k) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->seg_empty[k % kSegRing]);
@@ -448,8 +455,17 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                 const int used = min(w.a.cost() - at, left), b0 = max(0, at - kPairCost), b1 = max(0, at + used - kPairCost);
                 if (b0 < b1) {
                     if (!slot_free()) break;
+                    Seg &g = ctl->seg[k % kSegRing];
+                    for (int x = lane; x < w.a.rows; x += 32) {
+                        const int r = w.m * kPair + x, tok = group_div(p, r), hq = w.h * p.G + r - tok * p.G;
+                        const long long q_at = (w.r.t0 + tok) * p.q_t + hq * p.q_h;
+                        g.q_at[x] = (uint32_t)(q_at >> 3);
+                        g.o_at[x] = (uint32_t)(((w.r.t0 + tok) * p.o_t + hq * p.o_h) >> 3);
+                        prefetch_l2(p.q + q_at);  // its queries on their way to L2
+                        if (D == 128) prefetch_l2(p.q + q_at + 64);
+                    }
+                    __syncwarp();
                     if (lane == 0) {
-                        Seg &g = ctl->seg[k % kSegRing];
                         g.s = w.s;
                         g.h = w.h;
                         g.m = w.m;
@@ -486,13 +502,6 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     }
                     ++k;
                     first = false;
-                    // its queries on their way to L2
-                    for (int x = lane; x < w.a.rows; x += 32) {
-                        const int r = w.m * kPair + x, tok = group_div(p, r);
-                        const uint16_t *q = p.q + (w.r.t0 + tok) * p.q_t + (long long)(w.h * p.G + r - tok * p.G) * p.q_h;
-                        prefetch_l2(q);
-                        if (D == 128) prefetch_l2(q + 64);
-                    }
                 }
                 left -= used;
                 at = 0;
@@ -616,16 +625,16 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
         // ================================================ MMA issuer
         auto issuer = [&]() {
             const uint32_t id_s = idesc(kBlock, false), id_o = idesc(D, true);
-            const uint32_t o_tm = tmem + 256;
-            int n = 0;
-            uint32_t seg[2] = {0, 0}, step[2] = {0, 0};
+            int n = 0;  // ring blocks of the segments before
+            uint32_t seg[2] = {0, 0}, freed[2] = {0, 0}, given[2] = {0, 0};  // tile's segments, scores read, weights given
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 warp_wait(bar, parity);
                 fence_after();
                 return ok;
             };
-            auto s_mma = [&](int i, int st) {
-                const uint64_t a = desc_k(smem_u32(sq + i * S::BLOCK)), b = desc_k(smem_u32(ring + st * S::BLOCK));
+            auto copied = [&](int x) { return wait(&ctl->full[x % RING], (uint32_t)(x / RING)); };
+            auto s_mma = [&](int i, int x) {
+                const uint64_t a = desc_k(smem_u32(sq + i * S::BLOCK)), b = desc_k(smem_u32(ring + x % RING * S::BLOCK));
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint64_t off = (uint64_t)((k / 4) * (S::HALF >> 4) + (k % 4) * 2);
@@ -633,43 +642,71 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                 }
                 commit(&ctl->s_full[i]);
             };
+            auto pv_mma = [&](int i, int x, uint32_t acc) {
+                const uint64_t bv = desc_mn(smem_u32(ring + x % RING * S::BLOCK), S::HALF);
+#pragma unroll
+                for (int k = 0; k < kBlock / 16; ++k)
+                    mma_ts(tmem + S::O_COL + D * i, tmem + S::P_COL + S::P_TILE * i + S::P_HALF * (k / 4) + 8 * (k % 4),
+                           bv + (uint64_t)(k * (2048 >> 4)), id_o, k > 0 ? 1u : acc);
+                commit(&ctl->o_done[i]);
+            };
             for (uint32_t sg = 0; seg_begin(sg); ++sg) {
-                const int nt = ctl->seg[sg % kSegRing].rows > kTile ? 2 : 1;
-                int left = ctl->seg[sg % kSegRing].b1 - ctl->seg[sg % kSegRing].b0;
-                uint32_t acc = 0;
-                if (!wait(&ctl->full[n % RING], (uint32_t)(n / RING))) break;
-                for (int i = 0; i < nt; ++i) {
+                const int last_tile = ctl->seg[sg % kSegRing].rows > kTile ? 1 : 0;
+                const int nb = ctl->seg[sg % kSegRing].b1 - ctl->seg[sg % kSegRing].b0;
+                // ring block of the segment's j-th keys: n + 2 j, of its values: n + 2 j + 1
+                if (!copied(n)) break;
+                for (int i = 0; i <= last_tile; ++i) {
                     if (!wait(&ctl->q_ready[i], seg[i])) break;
                     ++seg[i];
                     issued = 1;
-                    s_mma(i, n % RING);
+                    s_mma(i, n);
                 }
                 if (!ok) break;
                 commit(&ctl->empty[n % RING]);
-                for (; left > 0; --left, n += 2, acc = 1) {
-                    const int sv = (n + 1) % RING, sk = (n + 2) % RING;
+                auto give = [&](int i, int j) {  // tile i's weights of block j times the values
+                    if (!wait(&ctl->p_full[i], given[i])) return false;
+                    ++given[i];
+                    pv_mma(i, n + 2 * j + 1, j > 0);
+                    if (i == last_tile) commit(&ctl->empty[(n + 2 * j + 1) % RING]);
+                    return true;
+                };
+                for (int j = 0; j < nb; ++j) {
                     // what the tensor cores need besides the weights is there long before them
-                    if (!wait(&ctl->full[sv], (uint32_t)((n + 1) / RING))) break;
-                    if (left > 1 && !wait(&ctl->full[sk], (uint32_t)((n + 2) / RING))) break;
-                    const uint64_t bv = desc_mn(smem_u32(ring + sv * S::BLOCK), S::HALF);
-                    for (int i = 0; i < nt; ++i) {
-                        if (!wait(&ctl->p_full[i], step[i])) break;
-                        ++step[i];
-#pragma unroll
-                        for (int k = 0; k < kBlock / 16; ++k)
-                            mma_ts(o_tm + D * i, tmem + 128 * i + 64 * (k / 4) + 8 * (k % 4), bv + (uint64_t)(k * (2048 >> 4)), id_o,
-                                   k > 0 ? 1u : acc);
-                        if (i == nt - 1) commit(&ctl->empty[sv]);
-                        if (left > 1) {
-                            s_mma(i, sk);
-                            if (i == nt - 1) commit(&ctl->empty[sk]);
-                        } else {
-                            commit(&ctl->o_full[i]);
+                    if (!copied(n + 2 * j + 1) || (j + 1 < nb && !copied(n + 2 * j + 2))) break;
+                    if constexpr (S::SPLIT) {
+                        // the next scores as soon as these have been read; the second tile half a step behind
+                        for (int i = 0; i <= last_tile; ++i) {
+                            if (j + 1 < nb) {
+                                if (!wait(&ctl->s_free[i], freed[i])) break;
+                                s_mma(i, n + 2 * j + 2);
+                                if (i == last_tile) commit(&ctl->empty[(n + 2 * j + 2) % RING]);
+                            } else if (!wait(&ctl->s_free[i], freed[i])) {
+                                break;
+                            }
+                            ++freed[i];
+                            if (last_tile == 0) {
+                                if (!give(0, j)) break;
+                            } else if (i == 0) {
+                                if (j > 0 && !give(1, j - 1)) break;
+                            } else if (!give(0, j)) {
+                                break;
+                            }
+                        }
+                        if (ok && last_tile && j + 1 == nb) give(1, j);
+                    } else {
+                        // the weights lie in the scores' place: the product first
+                        for (int i = 0; i <= last_tile; ++i) {
+                            if (!give(i, j)) break;
+                            if (j + 1 < nb) {
+                                s_mma(i, n + 2 * j + 2);
+                                if (i == last_tile) commit(&ctl->empty[(n + 2 * j + 2) % RING]);
+                            }
                         }
                     }
                     if (!ok) break;
                 }
                 if (!ok) break;
+                n += 2 * nb;
                 seg_end(sg);
             }
         };
@@ -687,10 +724,11 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             constexpr int U = D / 16;  // 16-byte units of half a row
             const int i = warp >> 3, half = (warp >> 2) & 1, row = tid & 127;
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-            // this thread's scores, and its weights in place of them (not of the other half's, whose
-            // thread may still be reading); its part of O
-            const uint32_t s_tm = tmem + 128 * i + 64 * half + lanes, p_tm = s_tm;
-            const uint32_t o_tm = tmem + 256 + D * i + D / 2 * half + lanes;
+            // this thread's scores; its weights (where they take the scores' place, then its own: the
+            // other half's thread may still be reading); its part of O
+            const uint32_t s_tm = tmem + 128 * i + 64 * half + lanes;
+            const uint32_t p_tm = tmem + S::P_COL + S::P_TILE * i + S::P_HALF * half + lanes;
+            const uint32_t o_tm = tmem + S::O_COL + D * i + D / 2 * half + lanes;
             uint64_t *x_ready = &ctl->x_ready[i][warp & 3];
             auto top_of = [&](uint32_t block, int h) -> volatile float & { return ctl->top[block & 3][i][h][row]; };
             uint32_t xs = 0;  // exchanges with the other half so far
@@ -706,7 +744,19 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                 const int x = half * U + u;
                 return reinterpret_cast<uint4 *>(sq + i * S::BLOCK + (x / 8) * S::HALF + r * 128 + (((x % 8) ^ (r & 7)) << 4));
             };
-            uint32_t step = 0, tseg = 0, kb = 0, n = 0;  // n: ring blocks before the current key block
+            uint32_t step = 0, kb = 0, n = 0;  // n: ring blocks before the current key block
+            uint4 qx[U];
+            bool held = false;  // qx holds the next segment's queries
+            auto load_q = [&](uint32_t k) {
+                const Seg &g = ctl->seg[k % kSegRing];
+#pragma unroll
+                for (int v = 0; v < U; ++v) {
+                    const int r = 32 * (warp & 3) + v * (32 / U) + lane / U;
+                    qx[v] = make_uint4(0u, 0u, 0u, 0u);
+                    if (i * kTile + r < g.rows)
+                        qx[v] = __ldg(reinterpret_cast<const uint4 *>(p.q) + g.q_at[i * kTile + r] + (half * U + lane % U));
+                }
+            };
             for (uint32_t sg = 0; seg_begin(sg); ++sg) {
                 const Seg &g = ctl->seg[sg % kSegRing];
                 const int r0 = g.m * kPair + i * kTile;  // the tile's first query row
@@ -718,26 +768,13 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     seg_end(sg);
                     continue;
                 }
-                // element offset of a tile row in q or out
-                auto offset = [&](int r, long long st, long long sh) {
-                    const int tok = group_div(p, r0 + r);
-                    return (g.t0 + tok) * st + (long long)(g.h * p.G + r0 + r - tok * p.G) * sh;
-                };
                 // queries: U lanes a row, so that a warp reads whole 64- or 128-byte runs
-                {
-                    uint4 x[U];
+                if (!held) load_q(sg);
 #pragma unroll
-                    for (int v = 0; v < U; ++v) {
-                        const int r = 32 * (warp & 3) + v * (32 / U) + lane / U;
-                        x[v] = make_uint4(0u, 0u, 0u, 0u);
-                        if (r < rows)
-                            x[v] = __ldg(reinterpret_cast<const uint4 *>(p.q + offset(r, p.q_t, p.q_h) + 8 * (half * U + lane % U)));
-                    }
-#pragma unroll
-                    for (int v = 0; v < U; ++v) *staged(32 * (warp & 3) + v * (32 / U) + lane / U, lane % U) = x[v];
-                    fence_proxy_async_smem();
-                    mbar_arrive(&ctl->q_ready[i]);
-                }
+                for (int v = 0; v < U; ++v) *staged(32 * (warp & 3) + v * (32 / U) + lane / U, lane % U) = qx[v];
+                held = false;
+                fence_proxy_async_smem();
+                mbar_arrive(&ctl->q_ready[i]);
                 const int lim = row < rows ? g.len - g.n + group_div(p, r0 + row) : -1;
                 const int all_hi = g.all_hi[i], all_lo = g.all_lo[i];
                 // rows that see nothing need no maximum
@@ -752,6 +789,10 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     const uint32_t mask = ctl->mask[kb % kMaskRing] >> (4 * half);
                     uint32_t x[64];
                     tld64(s_tm, x);
+                    if constexpr (S::SPLIT) {
+                        fence_before();
+                        mbar_arrive(&ctl->s_free[i]);
+                    }
                     if constexpr (I8) {
                         const float4 *ks = reinterpret_cast<const float4 *>(scale[0][kb % kMaskRing] + 64 * half);
 #pragma unroll
@@ -798,7 +839,9 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                         mx = nm;
                         l *= corr;
                         if (b > b0) {
-                            // the last P V is complete: it was issued before this block's S
+                            // the last P V must be complete (without SPLIT it was issued before this block's S)
+                            if (S::SPLIT && !warp_wait(&ctl->o_done[i], step - 2u)) break;
+                            fence_after();
 #pragma unroll 1
                             for (int d = 0; d < D / 2; d += 16) {
                                 uint32_t o[16];
@@ -818,6 +861,9 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                         if (!warp_wait(&ctl->full[(n + 1) % RING], (n + 1) / RING)) break;
                         vs = scale[1][kb % kMaskRing] + 64 * half;
                     }
+                    // the last weights have been used
+                    if (S::SPLIT && b > b0 && !warp_wait(&ctl->o_done[i], step - 2u)) break;
+                    if (S::SPLIT) fence_after();
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         uint32_t pk[16];
@@ -850,8 +896,13 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     top_of(kb, half) = top1;
                 }
                 // ---- the pair's output, or this piece's state
-                if (!ok || !warp_wait(&ctl->o_full[i], tseg)) break;
-                ++tseg;
+                if (!ok) break;
+                if (!seg_peek(sg + 1)) break;
+                if (i * kTile < ctl->seg[(sg + 1) % kSegRing].rows && ctl->seg[(sg + 1) % kSegRing].b1 > 0) {
+                    load_q(sg + 1);
+                    held = true;
+                }
+                if (!warp_wait(&ctl->o_done[i], step - 1u)) break;
                 fence_after();
                 l += exchange(kb, l);
                 if (!ok) break;
@@ -878,7 +929,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     for (int v = 0; v < U; ++v) {
                         const int r = 32 * (warp & 3) + v * (32 / U) + lane / U;
                         if (r < rows)
-                            *reinterpret_cast<uint4 *>(p.out + offset(r, p.o_t, p.o_h) + 8 * (half * U + lane % U)) = *staged(r, lane % U);
+                            reinterpret_cast<uint4 *>(p.out)[g.o_at[i * kTile + r] + (half * U + lane % U)] = *staged(r, lane % U);
                     }
                     __syncwarp();
                     uint32_t again = __ballot_sync(0xFFFFFFFFu, row < rows && !(sum < INFINITY) && g.n > 1);

@@ -692,8 +692,14 @@ tiles_status_t tiles_paged_attention(const tiles_paged_cache *cache, int32_t lay
         return TILES_ERR_UNSUPPORTED;
     if (n_tokens == 0) return TILES_OK;
     if (!q || !out || !al16(q) || !al16(out) || q_stride_token % 8 || q_stride_head % 8 || out_stride_token % 8 ||
-        out_stride_head % 8 || !workspace || !al16(workspace))
+        out_stride_head % 8 || q_stride_token < 0 || q_stride_head < 0 || out_stride_token < 0 || out_stride_head < 0 ||
+        !workspace || !al16(workspace))
         return TILES_ERR_INVALID_ARG;
+    // the kernels address q and out in 16-byte units of 32 bits
+    for (const int64_t *st : {&q_stride_token, &out_stride_token})
+        if ((double)n_tokens * (double)*st + (double)n_q_heads * (double)(st == &q_stride_token ? q_stride_head : out_stride_head) >=
+            8.0 * 4294967296.0)
+            return TILES_ERR_UNSUPPORTED;
     if (max_tokens > n_tokens) max_tokens = n_tokens;
     int sms = 0;
     if ((st = sm_count(&sms)) != TILES_OK) return st;
