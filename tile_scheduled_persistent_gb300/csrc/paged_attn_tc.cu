@@ -18,10 +18,10 @@
 //     when the softmax has turned S_i into weights in place, O_i += P_i V with P_i
 //     read from tensor memory. While one tile's rows are in the softmax the tensor
 //     cores work on the other tile.
-//   - two softmax warpgroups per tile, half a row of a block a thread: running
-//     maximum and sum in FP32; the halves exchange their maxima through shared memory.
-//     (One warpgroup, a row a thread: the chain from scores to weights took 1,700
-//     cycles and the tensor cores waited for it.) O_i is rescaled only when a row's maximum has risen by
+//   - the softmax of a row by one thread (D 64) or two (D 128, half a row each, as
+//     there the chain from scores to weights is what the tensor cores wait for;
+//     the halves exchange their maxima through shared memory): running maximum and sum
+//     in FP32. O_i is rescaled only when a row's maximum has risen by
 //     more than 8 powers of two since it was last set (weights stay below 2^8,
 //     which neither BF16 nor the FP32 sums mind), so hardly ever after the first
 //     block.
@@ -61,10 +61,14 @@ struct TcShape {
     static constexpr int HALF = kBlock * 128;           // bytes: 128 rows of 64 BF16
     static constexpr int BLOCK = HALF * (D / 64);       // one block of K or V, or a query tile
     static constexpr int RING = D == 128 ? 4 : 8;
-    // warpgroups: four of softmax; one of the MMA issuer, the loader (INT8: two warps) and the planner
-    static constexpr int THREADS = 640, LOADERS = I8 ? 64 : 32;
-    // registers a thread after the split: 4 x 104 + 64 = 5 x 96, the launch's
-    static constexpr int REG_SOFTMAX = 104, REG_ISSUE = 64;
+    // threads a query row's softmax is shared by
+    static constexpr int HALVES = D == 64 ? 1 : 2;
+    // warpgroups: HALVES of softmax for each tile; one of the MMA issuer, the loader (INT8: two
+    // warps) and the planner
+    static constexpr int SOFTMAX = 8 * HALVES, THREADS = (SOFTMAX + 4) * 32, LOADERS = I8 ? 64 : 32;
+    // registers a thread after the split; the sums are the launch's: 2 x 208 + 88 = 3 x 168 of
+    // 384 threads, 4 x 104 + 64 = 5 x 96 of 640
+    static constexpr int REG_SOFTMAX = HALVES == 1 ? 208 : 104, REG_ISSUE = HALVES == 1 ? 88 : 64;
     // tensor memory, 512 columns: scores of the two tiles (128 each), O (D each) and, at D 64,
     // room for the weights of their own; at D 128 they take the place of the scores
     static constexpr bool SPLIT = D == 64;
@@ -114,21 +118,37 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lead) {
 __device__ __forceinline__ uint32_t idesc(int n, bool b_mn) {  // M 128, BF16 x BF16 -> FP32
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
-// Executed by a whole converged warp; one lane, the same one every time, issues.
-// (Issued from a branch that a single lane takes, an MMA cost 190-240 cycles
-// whatever its size, as its descriptors then live in ordinary registers; this way
-// 64 of M 128, N 128, K 16, the tensor core's rate.)
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+// Four MMAs over 64 of the k index, executed by a whole converged warp; one lane,
+// the same one every time, issues. (Issued from a branch that a single lane takes,
+// an MMA cost 190-240 cycles whatever its size, as its descriptors then live in
+// ordinary registers; this way the tensor core's own rate, 64 cycles at M 128,
+// N 128, K 16.) SS: K-major A and B in shared memory, 32 bytes a step. TS: A in
+// tensor memory, 8 columns a step, MN-major B, 16 rows of 128 bytes a step.
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, t, e;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(id), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, t, e;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "add.s32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(id), "r"(acc)
         : "memory");
 }
@@ -324,16 +344,16 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
         mbar_init(&ctl->fix, 1);
         mbar_init(&ctl->drain, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&ctl->q_ready[i], 256);
+            mbar_init(&ctl->q_ready[i], 128 * S::HALVES);
             mbar_init(&ctl->s_full[i], 1);
-            mbar_init(&ctl->p_full[i], 256);
+            mbar_init(&ctl->p_full[i], 128 * S::HALVES);
             for (int k = 0; k < 4; ++k) mbar_init(&ctl->x_ready[i][k], 64);
-            mbar_init(&ctl->s_free[i], 256);
+            mbar_init(&ctl->s_free[i], 128 * S::HALVES);
             mbar_init(&ctl->o_done[i], 1);
         }
         for (int i = 0; i < kSegRing; ++i) {
             mbar_init(&ctl->seg_full[i], 1);
-            mbar_init(&ctl->seg_empty[i], 16 + 1 + S::LOADERS / 32);
+            mbar_init(&ctl->seg_empty[i], S::SOFTMAX + 1 + S::LOADERS / 32);
         }
         ctl->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -515,7 +535,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
         };
         // ================================================ loader
         auto loader = [&]() {
-            const int lt = tid - 17 * 32;  // thread of the loader
+            const int lt = tid - (S::SOFTMAX + 1) * 32;  // thread of the loader
             int n = 0;                     // blocks of K and V so far
             uint32_t kb = 0, fixes = 0;    // key blocks, repaired blocks so far
             for (uint32_t sk = 0; seg_begin(sk); ++sk) {
@@ -632,22 +652,19 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                 fence_after();
                 return ok;
             };
-            auto copied = [&](int x) { return wait(&ctl->full[x % RING], (uint32_t)(x / RING)); };
+            auto copied = [&](int x) { return warp_wait(&ctl->full[x % RING], (uint32_t)(x / RING)); };
             auto s_mma = [&](int i, int x) {
                 const uint64_t a = desc_k(smem_u32(sq + i * S::BLOCK)), b = desc_k(smem_u32(ring + x % RING * S::BLOCK));
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t off = (uint64_t)((k / 4) * (S::HALF >> 4) + (k % 4) * 2);
-                    mma_ss(tmem + 128 * i, a + off, b + off, id_s, k != 0);
-                }
+                for (int h = 0; h < D / 64; ++h) mma4_ss(tmem + 128 * i, a + h * (S::HALF >> 4), b + h * (S::HALF >> 4), id_s, h);
                 commit(&ctl->s_full[i]);
             };
             auto pv_mma = [&](int i, int x, uint32_t acc) {
                 const uint64_t bv = desc_mn(smem_u32(ring + x % RING * S::BLOCK), S::HALF);
 #pragma unroll
-                for (int k = 0; k < kBlock / 16; ++k)
-                    mma_ts(tmem + S::O_COL + D * i, tmem + S::P_COL + S::P_TILE * i + S::P_HALF * (k / 4) + 8 * (k % 4),
-                           bv + (uint64_t)(k * (2048 >> 4)), id_o, k > 0 ? 1u : acc);
+                for (int h = 0; h < 2; ++h)
+                    mma4_ts(tmem + S::O_COL + D * i, tmem + S::P_COL + S::P_TILE * i + S::P_HALF * h, bv + (uint64_t)(h * 512), id_o,
+                            h > 0 ? 1u : acc);
                 commit(&ctl->o_done[i]);
             };
             for (uint32_t sg = 0; seg_begin(sg); ++sg) {
@@ -656,7 +673,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                 // ring block of the segment's j-th keys: n + 2 j, of its values: n + 2 j + 1
                 if (!copied(n)) break;
                 for (int i = 0; i <= last_tile; ++i) {
-                    if (!wait(&ctl->q_ready[i], seg[i])) break;
+                    if (!warp_wait(&ctl->q_ready[i], seg[i])) break;
                     ++seg[i];
                     issued = 1;
                     s_mma(i, n);
@@ -711,28 +728,30 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             }
         };
         // ================================================ softmax, half a query row a thread
-        if (warp >= 16) {
+        if (warp >= S::SOFTMAX) {
             regs_down<S::REG_ISSUE>();
-            if (warp == 16)
+            if (warp == S::SOFTMAX)
                 issuer();
-            else if (warp == 19)
+            else if (warp == S::SOFTMAX + 3)
                 planner();
-            else if (I8 || warp == 17)
+            else if (I8 || warp == S::SOFTMAX + 1)
                 loader();
         } else {
             regs_up<S::REG_SOFTMAX>();
-            constexpr int U = D / 16;  // 16-byte units of half a row
-            const int i = warp >> 3, half = (warp >> 2) & 1, row = tid & 127;
+            // a thread's positions of a block, its dimensions of O, 16-byte units of those
+            constexpr int HV = S::HALVES, CW = kBlock / HV, DW = D / HV, U = DW / 8;
+            const int i = warp / (4 * HV), half = HV == 1 ? 0 : (warp >> 2) & 1, row = tid & 127;
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
             // this thread's scores; its weights (where they take the scores' place, then its own: the
             // other half's thread may still be reading); its part of O
-            const uint32_t s_tm = tmem + 128 * i + 64 * half + lanes;
+            const uint32_t s_tm = tmem + 128 * i + CW * half + lanes;
             const uint32_t p_tm = tmem + S::P_COL + S::P_TILE * i + S::P_HALF * half + lanes;
-            const uint32_t o_tm = tmem + S::O_COL + D * i + D / 2 * half + lanes;
+            const uint32_t o_tm = tmem + S::O_COL + D * i + DW * half + lanes;
             uint64_t *x_ready = &ctl->x_ready[i][warp & 3];
             auto top_of = [&](uint32_t block, int h) -> volatile float & { return ctl->top[block & 3][i][h][row]; };
             uint32_t xs = 0;  // exchanges with the other half so far
-            auto exchange = [&](uint32_t block, float v) {
+            auto exchange = [&](uint32_t block, float v, float alone) {  // the other half's value
+                if (HV == 1) return alone;
                 top_of(block, half) = v;
                 mbar_arrive(x_ready);
                 warp_wait(x_ready, xs);
@@ -784,19 +803,20 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     ++step;
                     fence_after();
                     // written before the other half's weights of the last block, so visible now
-                    const float other2 = b - b0 >= 2 ? top_of(kb + 2, half ^ 1) : -INFINITY;
-                    const int t0 = (b < g.nhb ? b : b - g.nhb + g.wb0) * kBlock + 64 * half;  // of this thread's positions
-                    const uint32_t mask = ctl->mask[kb % kMaskRing] >> (4 * half);
-                    uint32_t x[64];
-                    tld64(s_tm, x);
+                    const float other2 = HV == 2 && b - b0 >= 2 ? top_of(kb + 2, half ^ 1) : -INFINITY;
+                    const int t0 = (b < g.nhb ? b : b - g.nhb + g.wb0) * kBlock + CW * half;  // of this thread's positions
+                    const uint32_t mask = ctl->mask[kb % kMaskRing] >> (CW / 16 * half);
+                    uint32_t x[CW];
+#pragma unroll
+                    for (int j = 0; j < CW; j += 64) tld64(s_tm + j, reinterpret_cast<uint32_t(&)[64]>(x[j]));
                     if constexpr (S::SPLIT) {
                         fence_before();
                         mbar_arrive(&ctl->s_free[i]);
                     }
                     if constexpr (I8) {
-                        const float4 *ks = reinterpret_cast<const float4 *>(scale[0][kb % kMaskRing] + 64 * half);
+                        const float4 *ks = reinterpret_cast<const float4 *>(scale[0][kb % kMaskRing] + CW * half);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
+                        for (int j = 0; j < CW / 4; ++j) {
                             const float4 f = ks[j];
                             x[4 * j] = __float_as_uint(__uint_as_float(x[4 * j]) * f.x);
                             x[4 * j + 1] = __float_as_uint(__uint_as_float(x[4 * j + 1]) * f.y);
@@ -804,10 +824,10 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                             x[4 * j + 3] = __float_as_uint(__uint_as_float(x[4 * j + 3]) * f.w);
                         }
                     }
-                    if ((mask & 0xFu) != 0xFu || t0 + 63 > all_hi || t0 < all_lo) {
+                    if ((mask & low_bits(CW / 16)) != low_bits(CW / 16) || t0 + CW - 1 > all_hi || t0 < all_lo) {
                         // a bit per position (what is seen is a range of the row and the sinks)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
+                        for (int k = 0; k < CW / 32; ++k) {
                             const int tb = t0 + 32 * k;
                             uint32_t see = low_bits(lim + 1 - tb);
                             if (p.window > 0) see &= ~low_bits(lim - p.window + 1 - tb) | low_bits(p.sinks - tb);
@@ -820,18 +840,18 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     auto block_top = [&]() {
                         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int j = 0; j < 64; j += 8)
+                        for (int j = 0; j < CW; j += 8)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 m4[k] = max3(m4[k], __uint_as_float(x[j + k]), __uint_as_float(x[j + 4 + k]));
                         return max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * p.scale_log2;
                     };
                     // the row's reference: what both halves had seen two blocks ago
-                    const float seen = fmaxf(top2, other2);
+                    const float seen = HV == 1 ? top1 : fmaxf(top2, other2);
                     if (__any_sync(0xFFFFFFFFu, mx == -INFINITY || seen > mx + kRise)) {
                         float nm = seen > mx + kRise ? seen : mx;
                         if (__any_sync(0xFFFFFFFFu, mx == -INFINITY)) {  // rows that have seen nothing yet
-                            const float t = block_top(), u = fmaxf(t, exchange(kb, t));
+                            const float t = block_top(), u = fmaxf(t, exchange(kb, t, t));
                             if (!ok) break;
                             if (mx == -INFINITY) nm = u;
                         }
@@ -843,7 +863,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                             if (S::SPLIT && !warp_wait(&ctl->o_done[i], step - 2u)) break;
                             fence_after();
 #pragma unroll 1
-                            for (int d = 0; d < D / 2; d += 16) {
+                            for (int d = 0; d < DW; d += 16) {
                                 uint32_t o[16];
                                 tld16(o_tm + d, o);
 #pragma unroll
@@ -859,13 +879,13 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     if constexpr (I8) {
                         // the value block's scales: its copy is in once the block after the keys is full
                         if (!warp_wait(&ctl->full[(n + 1) % RING], (n + 1) / RING)) break;
-                        vs = scale[1][kb % kMaskRing] + 64 * half;
+                        vs = scale[1][kb % kMaskRing] + CW * half;
                     }
                     // the last weights have been used
                     if (S::SPLIT && b > b0 && !warp_wait(&ctl->o_done[i], step - 2u)) break;
                     if (S::SPLIT) fence_after();
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
+                    for (int q = 0; q < CW / 32; ++q) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
@@ -893,7 +913,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     l += l0 + l1;
                     top2 = top1;
                     top1 = block_top();
-                    top_of(kb, half) = top1;
+                    if (HV == 2) top_of(kb, half) = top1;
                 }
                 // ---- the pair's output, or this piece's state
                 if (!ok) break;
@@ -904,13 +924,13 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                 }
                 if (!warp_wait(&ctl->o_done[i], step - 1u)) break;
                 fence_after();
-                l += exchange(kb, l);
+                l += exchange(kb, l, 0.f);
                 if (!ok) break;
                 if (b0 == 0 && b1 == g.nb) {
                     const float inv = l == 0.f ? 0.f : 1.f / l;
                     float sum = 0.f;
 #pragma unroll 1
-                    for (int d = 0; d < D / 2; d += 16) {
+                    for (int d = 0; d < DW; d += 16) {
                         uint32_t o[16];
                         tld16(o_tm + d, o);
                         float v[16];
@@ -937,18 +957,18 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                         const int src = __ffs(again) - 1;
                         again &= again - 1;
                         // only this half's dimensions: the other half's warp sees to its own
-                        row_again<D, I8>(p, g.s, g.h, g.t0, g.n, g.len, r0 + 32 * (warp & 3) + src, D / 2 * half, D / 2 * half + D / 2);
+                        row_again<D, I8>(p, g.s, g.h, g.t0, g.n, g.len, r0 + 32 * (warp & 3) + src, DW * half, DW * half + DW);
                     }
                 } else {
                     float *dst = parts + (size_t)(2 * cta + g.slot) * S::PART;
                     const int pr = i * kTile + row;
 #pragma unroll 1
-                    for (int d = 0; d < D / 2; d += 16) {
+                    for (int d = 0; d < DW; d += 16) {
                         uint32_t o[16];
                         tld16(o_tm + d, o);
 #pragma unroll
                         for (int k = 0; k < 16; k += 4)
-                            *reinterpret_cast<uint4 *>(dst + (size_t)((D / 2 * half + d + k) / 4 * kPair + pr) * 4) =
+                            *reinterpret_cast<uint4 *>(dst + (size_t)((DW * half + d + k) / 4 * kPair + pr) * 4) =
                                 make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                     }
                     fence_before();
@@ -981,11 +1001,11 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
         if (lane == 0) atomicOr(reinterpret_cast<uint32_t *>(c.state), kDevTimeout);
         const unsigned long long d2 = global_timer() + kTimeoutNs;
         uint32_t never = 0;
-        if (warp == 16 && issued) {
+        if (warp == S::SOFTMAX && issued) {
             commit(&ctl->drain);
             bounded_wait(&ctl->drain, 0u, d2, &never);
         }
-        if (!I8 && warp == 17 && lane == 0)
+        if (!I8 && warp == S::SOFTMAX + 1 && lane == 0)
             for (int k = max(0, issued - RING); k < issued; ++k)
                 bounded_wait(&ctl->full[k % RING], (uint32_t)(k / RING) & 1u, d2, &never);
     }
