@@ -8,7 +8,10 @@ behind a row's end, or a masked position, shows.
 Tolerance of attention: |out - ref| <= 2^-8 |ref| (the output's rounding to
 BF16) + c sum_t w_t |v_t|, c = what the weights may be off by: the FP32 error of
 the scores (computed by the reference) + 2^-16 (weights enter the product as a
-BF16 high part and remainder) + 2^-20 (FP32 exponentials and sums).
+BF16 high part and remainder) + 2^-20 (FP32 exponentials and sums). With an INT8
+cache a weight times its value's scale enters as one FP16 number: half a step,
+2^-11, in the place of 2^-16 (and queries, scaled to below 2, are FP16: exact but
+for what lies under 2^-14 of the largest, 2^-25 absolute, which 2^-20 covers).
 """
 import itertools
 
@@ -51,7 +54,7 @@ class Case:
                  max_len=None, amp=1.0):
         import torch
         r = np.random.default_rng(seed)
-        self.lens, self.ns, self.hq, self.d = lens, ns, hq, d
+        self.lens, self.ns, self.hq, self.d, self.int8 = lens, ns, hq, d, int8
         width = -(-max(max(lens), 1, max_len or 0) // page)
         need = [-(-n // page) for n in lens]
         P = sum(need) + extra_pages
@@ -109,8 +112,10 @@ class Case:
                              sinks=sinks, **kw)
         return out
 
-    def check(self, out, window=0, sinks=0, weights=2.0 ** -16, scale=None):
+    def check(self, out, window=0, sinks=0, weights=None, scale=None):
         """weights: what a weight may be off by, before the scores' error."""
+        if weights is None:
+            weights = 2.0 ** -11 if self.int8 else 2.0 ** -16
         n = int(self.cu[-1])
         ref, spread, serr = R.attention(self.q[:n].double().cpu().numpy(), self.keys, self.values, self.lens, self.cu,
                                         self.d ** -0.5 if scale is None else scale, window, sinks)

@@ -346,6 +346,10 @@ class PagedKV:
             ("k_shift", k_shift))})
         self._ref = ctypes.byref(self._view)
         self._ws_bytes = {}
+        self._index, self._d, self._n_cu = self.device.index, d.head_dim, n_seqs + 1
+        self._i32, self._bf16, self._u8, self._empty = torch.int32, torch.bfloat16, torch.uint8, torch.empty
+        self._device_of, self._stream_of = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        self._scale, self._L = d.head_dim ** -0.5, _lib()
 
     def _values(self, buf, off: int):
         import torch
@@ -366,70 +370,68 @@ class PagedKV:
     def value_pool(self):
         return self._values(self.v, self.layout["v_scale_off"])
 
+    # The checks below run on every call of a decoding loop, so they ask PyTorch as
+    # little as they can: a tensor's device by its index, the stream by its handle.
     def _on(self, stream):
-        """The call's stream (default: torch's current one), once the cache's device is the current one."""
-        import torch
-        if self.device.index != torch.cuda.current_device():
+        """The call's stream handle (default: torch's current one); the cache's device must be the current one."""
+        if self._device_of() != self._index:
             raise TilesError(-4, "PagedKV: the cache lies on another device than the current one")
-        return ctypes.c_void_p((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+        return self._stream_of(self._index) if stream is None else stream.cuda_stream
 
     def _rows(self, t, what: str):
-        import torch
-        if t.dtype != torch.int32 or t.device != self.device or t.numel() != self.pdesc.n_seqs or not t.is_contiguous():
+        if t.dtype != self._i32 or t.get_device() != self._index or t.numel() != self.pdesc.n_seqs or \
+                not t.is_contiguous():
             raise TilesError(-1, f"{what}: int32 [n_seqs] on the cache's device")
         return t.data_ptr()
 
-    def _cu(self, t, n_tokens: int, what: str):
-        import torch
+    def _cu(self, t, what: str):
         if t is None:
             return None
-        if t.dtype != torch.int32 or t.device != self.device or t.numel() != self.pdesc.n_seqs + 1 or \
-                not t.is_contiguous():
+        if t.dtype != self._i32 or t.get_device() != self._index or t.numel() != self._n_cu or not t.is_contiguous():
             raise TilesError(-1, f"{what}: cu_tokens is int32 [n_seqs + 1] on the cache's device")
         return t.data_ptr()
 
-    def _heads(self, t, what: str, heads: int | None = None):
-        import torch
-        if t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != self.device or \
-                t.shape[2] != self.pdesc.head_dim or (t.stride(2) != 1 and t.numel()) or \
-                (heads is not None and t.shape[1] != heads):
+    def _heads(self, t, what: str):
+        """Shape and strides of a [tokens][heads][head_dim] tensor."""
+        shape, stride = t.shape, t.stride()
+        if len(shape) != 3 or t.dtype != self._bf16 or t.get_device() != self._index or shape[2] != self._d or \
+                (stride[2] != 1 and t.numel()):
             raise TilesError(-1, f"{what}: bfloat16 [tokens][heads][head_dim], head_dim contiguous, on the cache's device")
-        return t.data_ptr()
+        return shape, stride
 
     def reset(self, stream=None) -> None:
         """Empties the cache: no pages held, all lengths 0."""
-        _check(_lib().tiles_paged_reset(self._ref, self._on(stream)), "tiles_paged_reset")
+        _check(self._L.tiles_paged_reset(self._ref, self._on(stream)), "tiles_paged_reset")
 
     def resize(self, new_lens, stream=None) -> None:
         """Sets row lengths (int32 CUDA tensor [n_seqs]; negative: leave the row): pages are taken
         from the pool, given back, and copied where a growing row would write into a shared one."""
-        _check(_lib().tiles_paged_resize(self._ref, self._rows(new_lens, "tiles_paged_resize"), self._on(stream)),
+        _check(self._L.tiles_paged_resize(self._ref, self._rows(new_lens, "tiles_paged_resize"), self._on(stream)),
                "tiles_paged_resize")
 
     def fork(self, src_rows, stream=None) -> None:
         """Makes each empty row s with src_rows[s] >= 0 (int32 CUDA tensor [n_seqs]) share that row's pages."""
-        _check(_lib().tiles_paged_fork(self._ref, self._rows(src_rows, "tiles_paged_fork"), self._on(stream)),
+        _check(self._L.tiles_paged_fork(self._ref, self._rows(src_rows, "tiles_paged_fork"), self._on(stream)),
                "tiles_paged_fork")
 
     def trim(self, window: int, sinks: int = 0, stream=None) -> None:
         """Gives back the pages that no later token sees under this window and these sink positions."""
-        _check(_lib().tiles_paged_trim(self._ref, window, sinks, self._on(stream)), "tiles_paged_trim")
+        _check(self._L.tiles_paged_trim(self._ref, window, sinks, self._on(stream)), "tiles_paged_trim")
 
     def compact(self, stream=None) -> None:
         """Moves the pages in use to the front of the pool."""
-        _check(_lib().tiles_paged_compact(self._ref, self._on(stream)), "tiles_paged_compact")
+        _check(self._L.tiles_paged_compact(self._ref, self._on(stream)), "tiles_paged_compact")
 
     def append(self, layer: int, k, v, cu_tokens=None, stream=None) -> None:
         """Writes new K/V rows of a layer (BF16 CUDA tensors [tokens][n_kv_heads][head_dim], any token
         and head strides): row s has tokens cu_tokens[s] .. cu_tokens[s + 1] - 1 (int32 CUDA tensor, or
         None: one token a row) at its last positions."""
-        n = k.shape[0]
-        h = self.pdesc.n_kv_heads
-        kp, vp = self._heads(k, "tiles_paged_append", h), self._heads(v, "tiles_paged_append", h)
-        if v.shape[0] != n:
-            raise TilesError(-1, "tiles_paged_append: k and v have the same tokens")
-        _check(_lib().tiles_paged_append(self._ref, layer, kp, k.stride(0), k.stride(1), vp, v.stride(0), v.stride(1),
-                                         self._cu(cu_tokens, n, "tiles_paged_append"), n, self._on(stream)),
+        (n, h, _), ks = self._heads(k, "tiles_paged_append")
+        (nv, hv, _), vs = self._heads(v, "tiles_paged_append")
+        if nv != n or h != hv or h != self.pdesc.n_kv_heads:
+            raise TilesError(-1, "tiles_paged_append: k and v are [tokens][n_kv_heads][head_dim], of the same tokens")
+        _check(self._L.tiles_paged_append(self._ref, layer, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                                          self._cu(cu_tokens, "tiles_paged_append"), n, self._on(stream)),
                "tiles_paged_append")
 
     def workspace_bytes(self, n_q_heads: int, max_tokens: int = 1) -> int:
@@ -449,30 +451,31 @@ class PagedKV:
         `sinks`. cu_tokens as for append; max_tokens: a bound on a row's tokens; scale: default
         head_dim ** -0.5. workspace: a uint8 CUDA tensor of workspace_bytes (default: one is taken from
         PyTorch's allocator for the call)."""
-        import torch
-        n, heads = q.shape[0], q.shape[1]
-        qp, op = self._heads(q, "tiles_paged_attention"), self._heads(out, "tiles_paged_attention", heads)
-        if out.shape[0] != n:
-            raise TilesError(-1, "tiles_paged_attention: q and out have the same tokens")
+        (n, heads, _), qs = self._heads(q, "tiles_paged_attention")
+        shape, os_ = self._heads(out, "tiles_paged_attention")
+        if shape[0] != n or shape[1] != heads:
+            raise TilesError(-1, "tiles_paged_attention: q and out have the same tokens and heads")
         st = self._on(stream)
         if workspace is None:
-            need = self.workspace_bytes(heads, max_tokens)
+            need = self._ws_bytes.get((heads, max_tokens)) or self.workspace_bytes(heads, max_tokens)
             if stream is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+                workspace = self._empty(need, dtype=self._u8, device=self.device)
             else:
+                import torch
                 with torch.cuda.stream(stream):
-                    workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-        elif workspace.device != self.device or not workspace.is_contiguous():
+                    workspace = self._empty(need, dtype=self._u8, device=self.device)
+        elif workspace.get_device() != self._index or not workspace.is_contiguous():
             raise TilesError(-1, "tiles_paged_attention: the workspace is contiguous, on the cache's device")
-        _check(_lib().tiles_paged_attention(
-            self._ref, layer, heads, qp, q.stride(0), q.stride(1), op, out.stride(0), out.stride(1),
-            self._cu(cu_tokens, n, "tiles_paged_attention"), n, max_tokens,
-            self.pdesc.head_dim ** -0.5 if scale is None else scale, window, sinks, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), st), "tiles_paged_attention")
+        else:
+            need = workspace.numel() * workspace.element_size()
+        _check(self._L.tiles_paged_attention(
+            self._ref, layer, heads, q.data_ptr(), qs[0], qs[1], out.data_ptr(), os_[0], os_[1],
+            self._cu(cu_tokens, "tiles_paged_attention"), n, max_tokens, self._scale if scale is None else scale, window,
+            sinks, workspace.data_ptr(), need, st), "tiles_paged_attention")
 
     def status(self, stream=None) -> int:
         """Synchronises and returns (and clears) what the calls recorded on the device."""
-        return _lib().tiles_paged_status(self._ref, self._on(stream))
+        return self._L.tiles_paged_status(self._ref, self._on(stream))
 
     def check(self, stream=None) -> None:
         _check(self.status(stream), "tiles_paged_status")

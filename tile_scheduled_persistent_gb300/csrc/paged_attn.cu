@@ -22,6 +22,13 @@
 // rescaled only when a maximum rises. Weights enter the P V product as a BF16
 // high part plus a BF16 remainder (2^-17 relative), so the result is FP32-exact
 // up to the output's rounding; the extra MMAs are free in a memory-bound kernel.
+//
+// INT8 cache: the codes are widened to FP16 (exactly: a byte permute and one
+// subtraction a pair), so the MMAs take FP16. Queries are scaled by a power of two
+// to below 2 (exact; what falls under 2^-24 of the largest is rounded). A weight
+// times its value's scale enters as one FP16 number, 2^12 at most and relative to a
+// power of two not below the largest scale so far: 2^-12 relative, 2^-37 of the
+// largest absolute. Widening is what bounds this form, hence no remainder here.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -33,8 +40,12 @@ namespace paged {
 
 constexpr int kWarps = 4;
 constexpr int kThr = kWarps * 32;
-constexpr int kCtasPerSm = 3;
-constexpr int kMinUnits = kWarps;  // a CTA's piece is at least one unit a warp
+// CTAs an SM: what 168 registers a thread allow, 128 for an INT8 cache (half the bytes in
+// flight a warp, but more warps to widen codes while others wait)
+constexpr int ctas_per_sm(bool i8) { return i8 ? 4 : 3; }
+// The line counts an item as its units and kItemCost for its queries, its first loads and
+// its merge (about 4 us, in which a CTA takes 8 units); a piece is at least kMinCost.
+constexpr int kItemCost = 8, kMinCost = kWarps;
 
 // What a CTA leaves about the item that it began and others finish: the number
 // of partial states (0: none), the item, the slot of its own one.
@@ -54,14 +65,33 @@ __device__ __forceinline__ uint2 ld_stream8(const uint8_t *p) {
     asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
     return v;
 }
-// The INT8 codes in bytes 0 and 2 of y (bytes 1 and 3: anything) as a BF16
-// pair, exactly: (0x43, c & 127) - (0x43, c & 128) as BF16 numbers is c.
-__device__ __forceinline__ uint32_t pair_codes(uint32_t y) {
+// INT8 codes as FP16 numbers, exactly: the byte c + 128 below 0x64 is 1024 + (c + 128),
+// and 1152 less is c. half_codes: bytes 0 and 2 of the two halves already under 0x64.
+__device__ __forceinline__ uint32_t half_codes(uint32_t biased) {
     uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;"
-        : "=r"(r)
-        : "r"((y & 0x007F007Fu) | 0x43004300u), "r"((y & 0x00800080u) | 0x43004300u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(biased), "r"(0x64806480u));
     return r;
+}
+__device__ __forceinline__ uint32_t cvt_h2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// mma_rows8 and mma_m16n8k16 with FP16 operands
+__device__ __forceinline__ void mma_rows8_h(float &c0, float &c1, uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+    asm volatile("{\n\t.reg .f32 z2, z3;\n\t"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, z2, z3}, {%2, %6, %3, %6}, {%4, %5},"
+        " {%0, %1, %7, %7};\n\t}"
+        : "+f"(c0), "+f"(c1)
+        : "r"(a0), "r"(a2), "r"(b0), "r"(b1), "r"(0u), "f"(0.f));
+}
+__device__ __forceinline__ void mma_m16n8k16_h(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+        " {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // One (row, KV head, query tile) item's geometry.
@@ -69,6 +99,7 @@ struct Item {
     int t0, n, len;       // first token, tokens, length
     int head, lo;         // positions seen by some token: [0, head) and [lo, len)
     int nhu, wu0, nb;     // units of the head part, first unit of the rest, units in all
+    __device__ __forceinline__ int cost() const { return nb ? nb + kItemCost : 0; }
 };
 template <int UP>
 __device__ __forceinline__ Item item_of(const AttnParams &p, int s, bool *bad) {
@@ -88,7 +119,7 @@ __device__ __forceinline__ Item item_of(const AttnParams &p, int s, bool *bad) {
 template <int D, bool I8, int RT>
 struct Shape {
     static constexpr int EB = I8 ? 1 : 2;
-    static constexpr int NB = I8 ? 256 / D : 128 / D;  // 16-position blocks a unit
+    static constexpr int NB = 128 / D;                 // 16-position blocks a unit
     static constexpr int UP = 16 * NB;                 // positions a unit
     static constexpr int KC = D * EB / 64;             // 64-byte groups of a key row
     static constexpr int VW = I8 && D == 128 ? 16 : 8; // dimensions a lane takes of a value row and chunk
@@ -99,7 +130,7 @@ struct Shape {
 };
 
 template <int D, bool I8, int RT>
-__global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kThr, ctas_per_sm(I8)) stream_kernel(const __grid_constant__ AttnParams p) {
     using S = Shape<D, I8, RT>;
     constexpr int NB = S::NB, UP = S::UP, RH = S::RH, LD = S::LD;
     __shared__ long long wsum[kWarps];
@@ -121,7 +152,7 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
     for (int s = sa; s < sb; ++s) {
         bool bad = false;
         const Item it = item_of<UP>(p, s, &bad);
-        mine += (long long)it.nb * tiles_of(it) * c.nkv;
+        mine += (long long)it.cost() * tiles_of(it) * c.nkv;
     }
     long long x = mine;
 #pragma unroll
@@ -137,8 +168,8 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
         if (w < warp) before += wsum[w];
         total += wsum[w];
     }
-    // pieces: as many as there are CTAs, but of no fewer than kMinUnits units
-    const long long nc = min((long long)p.ctas, max(1ll, total / kMinUnits));
+    // pieces: as many as there are CTAs, but not too small
+    const long long nc = min((long long)p.ctas, max(1ll, total / kMinCost));
     const bool works = cta < nc && total > 0;
     const long long begin = works ? cta * total / nc : 0, end = works ? (cta + 1) * total / nc : 0;
     if (begin < end) {
@@ -148,7 +179,7 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
             for (; s < sb; ++s) {
                 bool bad = false;
                 const Item it = item_of<UP>(p, s, &bad);
-                const long long u = (long long)it.nb * tiles_of(it) * c.nkv;
+                const long long u = (long long)it.cost() * tiles_of(it) * c.nkv;
                 if (begin < at + u) break;
                 at += u;
             }
@@ -159,25 +190,33 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
         int s = found[0];
         long long at = found_at;  // line position of row s's first unit
         long long pos = begin;
+        bool first = true;  // no item with units so far
         while (pos < end) {
             bool bad = false;
             const Item it = item_of<UP>(p, s, &bad);
             const int nt = tiles_of(it);
-            const long long row_units = (long long)it.nb * nt * c.nkv;
+            const int cost = it.cost();
+            const long long row_units = (long long)cost * nt * c.nkv;
             if (pos >= at + row_units) {
                 at += row_units;
                 ++s;
                 continue;
             }
-            const int idx = (int)((pos - at) / it.nb), h = idx / nt, tile = idx - h * nt;
-            const long long item_at = at + (long long)idx * it.nb;
-            const int b0 = (int)(pos - item_at), b1 = (int)min((long long)it.nb, end - item_at);
+            const int idx = (int)((pos - at) / cost), h = idx / nt, tile = idx - h * nt;
+            // of an item that begins at cost unit 0, cost unit kItemCost + b is unit b
+            const long long item_at = at + (long long)idx * cost, upto = min(item_at + cost, end);
+            const int b0 = max(0, (int)(pos - item_at) - kItemCost), b1 = (int)(upto - item_at) - kItemCost;
+            if (b1 <= b0) {  // only the item's first cost units: the next CTA begins it
+                pos = upto;
+                continue;
+            }
             const int r0 = tile * RT, rows = min(RT, it.n * p.G - r0);
             const int32_t *table = c.tables + (size_t)s * c.width;
 
             // ---- queries of rows g (and g + 8) in the MMA's k order
             uint32_t qf[RH][S::NS][2];
             int lim[RH];
+            float qs[RH];  // INT8: the scores' factor besides the key's scale
 #pragma unroll
             for (int rr = 0; rr < RH; ++rr) {
                 const int r = r0 + g + 8 * rr;
@@ -198,6 +237,27 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
                         qf[rr][2 * i + 1][1] = w.w;
                     }
                 }
+                if constexpr (I8) {
+                    float amax = 0.f;
+#pragma unroll
+                    for (int i = 0; i < S::NS; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            amax = fmaxf(amax, fmaxf(fabsf(bf_lo(qf[rr][i][e])), fabsf(bf_hi(qf[rr][i][e]))));
+                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+                    const uint32_t ex = min(max(__float_as_uint(amax) >> 23, 1u), 253u);
+                    const float f = __uint_as_float((254u - ex) << 23);
+                    qs[rr] = p.scale_log2 * __uint_as_float(ex << 23);
+                    // codes 0 and 2 of a word are one register, 1 and 3 the other: so are the queries
+#pragma unroll
+                    for (int i = 0; i < S::NS; ++i) {
+                        const float f0 = bf_lo(qf[rr][i][0]) * f, f1 = bf_hi(qf[rr][i][0]) * f, f2 = bf_lo(qf[rr][i][1]) * f,
+                                    f3 = bf_hi(qf[rr][i][1]) * f;
+                        qf[rr][i][0] = cvt_h2(f0, f2);
+                        qf[rr][i][1] = cvt_h2(f1, f3);
+                    }
+                }
             }
             // positions every row sees: up to the first row's limit, from the last row's window on
             const int p_first = it.len - it.n + r0 / p.G, p_last = it.len - it.n + (r0 + rows - 1) / p.G;
@@ -214,18 +274,19 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
                 l[rr] = 0.f;
             }
 
+            float vref = 0x1p-100f;  // INT8: what the weights' value scales are relative to, a power of two
             uint4 kr[NB][2][S::KC], vr[NB][4][S::VC];
             float2 ksc[I8 ? NB : 1][2], vsc[I8 ? NB : 1][2];
             auto unit_t0 = [&](int b) { return (b < it.nhu ? b : b - it.nhu + it.wu0) * UP; };
-            // pool row of position tb (a multiple of 16), or -1: outside the length, or no page
-            auto pool_row = [&](int tb) -> long long {
+            // the pool's group of 16 rows with position tb (a multiple of 16); -1: outside the length, -2: no page
+            auto pool_group = [&](int tb) {
                 if (tb >= it.len) return -1;
                 const int page = __ldg(table + (tb >> c.psl));
                 if (page < 0 || page >= c.n_pages) return -2;
-                return ((long long)page * c.nkv + h) * c.ps + (tb & (c.ps - 1));
+                return ((page * c.nkv + h) << (c.psl - 4)) + ((tb & (c.ps - 1)) >> 4);
             };
-            long long krow[NB], nrow[NB];
-            auto load_k = [&](const long long (&row)[NB]) {
+            int krow[NB], nrow[NB];
+            auto load_k = [&](const int (&row)[NB]) {
 #pragma unroll
                 for (int i = 0; i < NB; ++i)
 #pragma unroll
@@ -235,16 +296,16 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
                             kr[i][a][cc] = make_uint4(0u, 0u, 0u, 0u);
                             if (row[i] >= 0)
                                 kr[i][a][cc] =
-                                    ld_stream16(c.k + (row[i] + 8 * a + g) * (D * S::EB) + 64 * cc + 16 * t4);
+                                    ld_stream16(c.k + (row[i] * 16ll + 8 * a + g) * (D * S::EB) + 64 * cc + 16 * t4);
                         }
                         if constexpr (I8) {
                             ksc[i][a] = make_float2(0.f, 0.f);
                             if (row[i] >= 0)
-                                ksc[i][a] = __ldg(reinterpret_cast<const float2 *>(c.ks + row[i] + 8 * a + 2 * t4));
+                                ksc[i][a] = __ldg(reinterpret_cast<const float2 *>(c.ks + row[i] * 16ll + 8 * a + 2 * t4));
                         }
                     }
             };
-            auto load_v = [&](const long long (&row)[NB]) {
+            auto load_v = [&](const int (&row)[NB]) {
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
 #pragma unroll
@@ -253,7 +314,7 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
                         for (int cc = 0; cc < S::VC; ++cc) {
                             vr[i][a][cc] = make_uint4(0u, 0u, 0u, 0u);
                             if (row[i] >= 0) {
-                                const uint8_t *v = c.v + (row[i] + 2 * t4 + (a & 1) + 8 * (a >> 1)) * (D * S::EB);
+                                const uint8_t *v = c.v + (row[i] * 16ll + 2 * t4 + (a & 1) + 8 * (a >> 1)) * (D * S::EB);
                                 if constexpr (I8 && D == 64) {
                                     const uint2 w = ld_stream8(v + 8 * g);
                                     vr[i][a][cc].x = w.x;
@@ -268,7 +329,7 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
                         for (int a = 0; a < 2; ++a) {
                             vsc[i][a] = make_float2(0.f, 0.f);
                             if (row[i] >= 0)
-                                vsc[i][a] = __ldg(reinterpret_cast<const float2 *>(c.vs + row[i] + 8 * a + 2 * t4));
+                                vsc[i][a] = __ldg(reinterpret_cast<const float2 *>(c.vs + row[i] * 16ll + 8 * a + 2 * t4));
                         }
                     }
                 }
@@ -276,7 +337,7 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
 
             if (b0 + warp < b1) {
 #pragma unroll
-                for (int i = 0; i < NB; ++i) krow[i] = pool_row(unit_t0(b0 + warp) + 16 * i);
+                for (int i = 0; i < NB; ++i) krow[i] = pool_group(unit_t0(b0 + warp) + 16 * i);
                 load_k(krow);
             }
             for (int b = b0 + warp; b < b1; b += kWarps) {
@@ -285,7 +346,7 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
                 const bool more = b + kWarps < b1;
                 if (more) {
 #pragma unroll
-                    for (int i = 0; i < NB; ++i) nrow[i] = pool_row(unit_t0(b + kWarps) + 16 * i);
+                    for (int i = 0; i < NB; ++i) nrow[i] = pool_group(unit_t0(b + kWarps) + 16 * i);
                 }
                 // ---- scores
                 float sc[NB][2][2 * RH];
@@ -299,28 +360,30 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
                             const uint32_t w[4] = {kr[i][a][cc].x, kr[i][a][cc].y, kr[i][a][cc].z, kr[i][a][cc].w};
 #pragma unroll
                             for (int st = 0; st < (I8 ? 4 : 2); ++st) {
-                                uint32_t k0, k1;
                                 const int q = cc * (I8 ? 4 : 2) + st;
                                 if constexpr (I8) {
-                                    codes_bf16x2(w[st], k0, k1);
+                                    const uint32_t x = w[st] ^ 0x80808080u;
+                                    const uint32_t k0 = half_codes(__byte_perm(x, 0x64646464u, 0x4240));
+                                    const uint32_t k1 = half_codes(__byte_perm(x, 0x64646464u, 0x4341));
+                                    if constexpr (RH == 1)
+                                        mma_rows8_h(acc[0], acc[1], qf[0][q][0], qf[0][q][1], k0, k1);
+                                    else
+                                        mma_m16n8k16_h(acc, qf[0][q][0], qf[RH - 1][q][0], qf[0][q][1], qf[RH - 1][q][1], k0, k1);
+                                } else if constexpr (RH == 1) {
+                                    mma_rows8(acc[0], acc[1], qf[0][q][0], qf[0][q][1], w[2 * st], w[2 * st + 1]);
                                 } else {
-                                    k0 = w[2 * st];
-                                    k1 = w[2 * st + 1];
+                                    mma_m16n8k16(acc, qf[0][q][0], qf[RH - 1][q][0], qf[0][q][1], qf[RH - 1][q][1], w[2 * st],
+                                                 w[2 * st + 1]);
                                 }
-                                if constexpr (RH == 1)
-                                    mma_rows8(acc[0], acc[1], qf[0][q][0], qf[0][q][1], k0, k1);
-                                else
-                                    mma_m16n8k16(acc, qf[0][q][0], qf[RH - 1][q][0], qf[0][q][1], qf[RH - 1][q][1], k0,
-                                                 k1);
                             }
                         }
-                        float f0 = p.scale_log2, f1 = f0;
-                        if constexpr (I8) {
-                            f0 *= ksc[i][a].x;
-                            f1 *= ksc[i][a].y;
-                        }
 #pragma unroll
-                        for (int e = 0; e < 2 * RH; ++e) sc[i][a][e] = acc[e] * (e & 1 ? f1 : f0);
+                        for (int e = 0; e < 2 * RH; ++e) {
+                            if constexpr (I8)
+                                sc[i][a][e] = acc[e] * (qs[e / 2] * (e & 1 ? ksc[i][a].y : ksc[i][a].x));
+                            else
+                                sc[i][a][e] = acc[e] * p.scale_log2;
+                        }
                     }
                 if (more) load_k(nrow);
                 // ---- mask, where some row does not see all of the unit
@@ -368,12 +431,29 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
                     mn[rr] = fmaxf(m[rr], mx);
                     rise |= mn[rr] > m[rr];
                 }
+                float vscale = 1.f;
+                if constexpr (I8) {
+                    float vmax = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NB; ++i)
+#pragma unroll
+                        for (int a = 0; a < 2; ++a) vmax = fmaxf(vmax, fmaxf(vsc[i][a].x, vsc[i][a].y));
+                    vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, 1));
+                    vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, 2));
+                    if (vmax > vref) {  // the same in all lanes
+                        const float nv = __uint_as_float(min((__float_as_uint(vmax) + 0x007FFFFFu) & 0x7F800000u, 0x7F000000u));
+                        vscale = vref / nv;
+                        vref = nv;
+                        rise = true;
+                    }
+                }
                 if (__any_sync(0xFFFFFFFFu, rise)) {
 #pragma unroll
                     for (int rr = 0; rr < RH; ++rr) {
-                        const float corr = mn[rr] > m[rr] ? ex2(m[rr] - mn[rr]) : 1.f;
+                        float corr = mn[rr] > m[rr] ? ex2(m[rr] - mn[rr]) : 1.f;
                         m[rr] = mn[rr];
                         l[rr] *= corr;
+                        corr *= vscale;
 #pragma unroll
                         for (int j = 0; j < S::VC * S::VW; ++j) {
                             o[j][2 * rr] *= corr;
@@ -391,15 +471,16 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
                     for (int a = 0; a < 2; ++a)
 #pragma unroll
                         for (int rr = 0; rr < RH; ++rr) {
-                            float w0 = ex2(sc[i][a][2 * rr] - base[rr]), w1 = ex2(sc[i][a][2 * rr + 1] - base[rr]);
+                            const float w0 = ex2(sc[i][a][2 * rr] - base[rr]), w1 = ex2(sc[i][a][2 * rr + 1] - base[rr]);
                             l[rr] += w0 + w1;
                             if constexpr (I8) {
-                                w0 *= vsc[i][a].x;
-                                w1 *= vsc[i][a].y;
+                                const float f = 4096.f / vref;
+                                ph[rr][a] = cvt_h2(w0 * (vsc[i][a].x * f), w1 * (vsc[i][a].y * f));
+                            } else {
+                                const uint32_t hi = cvt_bf2(w0, w1);
+                                ph[rr][a] = hi;
+                                pl[rr][a] = cvt_bf2(w0 - bf_lo(hi), w1 - bf_hi(hi));
                             }
-                            const uint32_t hi = cvt_bf2(w0, w1);
-                            ph[rr][a] = hi;
-                            pl[rr][a] = cvt_bf2(w0 - bf_lo(hi), w1 - bf_hi(hi));
                         }
                     // ---- o += P V, one 8-column tile per dimension a lane holds
 #pragma unroll
@@ -408,27 +489,42 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
                                                   {vr[i][1][cc].x, vr[i][1][cc].y, vr[i][1][cc].z, vr[i][1][cc].w},
                                                   {vr[i][2][cc].x, vr[i][2][cc].y, vr[i][2][cc].z, vr[i][2][cc].w},
                                                   {vr[i][3][cc].x, vr[i][3][cc].y, vr[i][3][cc].z, vr[i][3][cc].w}};
+                        if constexpr (I8) {
 #pragma unroll
-                        for (int j = 0; j < S::VW; ++j) {
-                            uint32_t v0, v1;
-                            if constexpr (I8) {
-                                // the codes of rows a and b in the low bytes of two halves, then to
-                                // BF16 as codes_bf16x2 does
-                                const uint32_t sel = 0x0400u + 0x0101u * (j % 4);
-                                v0 = pair_codes(__byte_perm(w[0][j / 4], w[1][j / 4], sel));
-                                v1 = pair_codes(__byte_perm(w[2][j / 4], w[3][j / 4], sel));
-                            } else {
-                                const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
-                                v0 = __byte_perm(w[0][j / 2], w[1][j / 2], sel);
-                                v1 = __byte_perm(w[2][j / 2], w[3][j / 2], sel);
+                            for (int q = 0; q < S::VW / 4; ++q) {
+                                const uint32_t x0 = w[0][q] ^ 0x80808080u, x1 = w[1][q] ^ 0x80808080u;
+                                const uint32_t x2 = w[2][q] ^ 0x80808080u, x3 = w[3][q] ^ 0x80808080u;
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    // the codes of two dimensions in rows (0, 1) and (2, 3)
+                                    const uint32_t y0 = __byte_perm(x0, x1, h ? 0x7362 : 0x5140);
+                                    const uint32_t y1 = __byte_perm(x2, x3, h ? 0x7362 : 0x5140);
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) {
+                                        const uint32_t v0 = half_codes(__byte_perm(y0, 0x64646464u, e ? 0x4342 : 0x4140));
+                                        const uint32_t v1 = half_codes(__byte_perm(y1, 0x64646464u, e ? 0x4342 : 0x4140));
+                                        float(&oj)[2 * RH] = o[cc * S::VW + 4 * q + 2 * h + e];
+                                        if constexpr (RH == 1)
+                                            mma_rows8_h(oj[0], oj[1], ph[0][0], ph[0][1], v0, v1);
+                                        else
+                                            mma_m16n8k16_h(oj, ph[0][0], ph[1][0], ph[0][1], ph[1][1], v0, v1);
+                                    }
+                                }
                             }
-                            float(&oj)[2 * RH] = o[cc * S::VW + j];
-                            if constexpr (RH == 1) {
-                                mma_rows8(oj[0], oj[1], ph[0][0], ph[0][1], v0, v1);
-                                mma_rows8(oj[0], oj[1], pl[0][0], pl[0][1], v0, v1);
-                            } else {
-                                mma_m16n8k16(oj, ph[0][0], ph[1][0], ph[0][1], ph[1][1], v0, v1);
-                                mma_m16n8k16(oj, pl[0][0], pl[1][0], pl[0][1], pl[1][1], v0, v1);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < S::VW; ++j) {
+                                const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
+                                const uint32_t v0 = __byte_perm(w[0][j / 2], w[1][j / 2], sel);
+                                const uint32_t v1 = __byte_perm(w[2][j / 2], w[3][j / 2], sel);
+                                float(&oj)[2 * RH] = o[cc * S::VW + j];
+                                if constexpr (RH == 1) {
+                                    mma_rows8(oj[0], oj[1], ph[0][0], ph[0][1], v0, v1);
+                                    mma_rows8(oj[0], oj[1], pl[0][0], pl[0][1], v0, v1);
+                                } else {
+                                    mma_m16n8k16(oj, ph[0][0], ph[1][0], ph[0][1], ph[1][1], v0, v1);
+                                    mma_m16n8k16(oj, pl[0][0], pl[1][0], pl[0][1], pl[1][1], v0, v1);
+                                }
                             }
                         }
                     }
@@ -440,6 +536,13 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
             }
 
             // ---- merge the warps' states
+            if constexpr (I8) {
+                const float f = vref / 4096.f;
+#pragma unroll
+                for (int j = 0; j < S::VC * S::VW; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2 * RH; ++e) o[j][e] *= f;
+            }
 #pragma unroll
             for (int rr = 0; rr < RH; ++rr) {
                 l[rr] += __shfl_xor_sync(0xFFFFFFFFu, l[rr], 1);
@@ -464,9 +567,10 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
             if (tid < RT) again[tid] = 0;
             __syncthreads();
             const bool whole = b0 == 0 && b1 == it.nb;
-            const int slot = pos == begin ? 0 : 1;
+            const int slot = first ? 0 : 1;
+            first = false;
             if (!whole && b0 == 0 && tid == 0) {
-                const long long last = ((item_at + it.nb) * nc + total - 1) / total - 1;  // the CTA with the item's end
+                const long long last = ((item_at + cost) * nc + total - 1) / total - 1;  // the CTA with the item's end
                 JoinRec r;
                 r.parts = (int)(last - cta) + 1;
                 r.s = s;
@@ -518,7 +622,7 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_c
             if (whole && it.n > 1)
                 for (int r = warp; r < rows; r += kWarps)
                     if (again[r]) row_again<D, I8>(p, s, h, it.t0, it.n, it.len, r0 + r);
-            pos = item_at + b1;
+            pos = upto;
         }
     }
     // ---- rows that see nothing, and rows that break the rules
@@ -544,9 +648,8 @@ template <int D, bool I8, int RT>
 __global__ void __launch_bounds__(kThr) join_kernel(const __grid_constant__ AttnParams p) {
     using S = Shape<D, I8, RT>;
     constexpr int LD = S::LD, TPR = D / 4, GR = kThr / TPR;
-    __shared__ float mx[kWarps];
     __shared__ __align__(16) float4 so[GR][TPR];
-    __shared__ float sl[GR];
+    __shared__ float2 sl[GR];
     __shared__ int bad_row;
     const int tid = threadIdx.x, cta = blockIdx.x, r = blockIdx.y;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -558,41 +661,62 @@ __global__ void __launch_bounds__(kThr) join_kernel(const __grid_constant__ Attn
     if (row >= it.n * p.G) return;
     const float *parts = p.ws + (size_t)p.ctas * (sizeof(JoinRec) / 4) + (size_t)r * LD;
     auto part = [&](int i) { return parts + (size_t)(2 * (cta + i) + (i == 0 ? rec.slot : 0)) * RT * LD; };
-    float M = -INFINITY;
-    for (int i = tid; i < rec.parts; i += kThr) M = fmaxf(M, __ldcg(part(i) + D));
-    M = warp_max(M);
-    if ((tid & 31) == 0) mx[tid >> 5] = M;
-    if (tid == 0) bad_row = 0;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mx[w]);
-    const float bs = M == -INFINITY ? 0.f : M;
+    // a group's own running maximum, so that states and maxima are read at once
     const int grp = tid / TPR, d0 = (tid % TPR) * 4;
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f;
-#pragma unroll 4
-    for (int i = grp; i < rec.parts; i += GR) {
-        const float *q = part(i);
-        const float f = ex2(__ldcg(q + D) - bs);
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(q + d0));
-        L = fmaf(f, __ldcg(q + D + 1), L);
-        O.x = fmaf(f, v.x, O.x);
-        O.y = fmaf(f, v.y, O.y);
-        O.z = fmaf(f, v.z, O.z);
-        O.w = fmaf(f, v.w, O.w);
+    float L = 0.f, M = -INFINITY;
+    for (int i0 = grp; i0 < rec.parts; i0 += 4 * GR) {
+        float4 v[4];
+        float2 ml[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * GR;
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (i < rec.parts) {
+                ml[k] = __ldcg(reinterpret_cast<const float2 *>(part(i) + D));
+                v[k] = __ldcg(reinterpret_cast<const float4 *>(part(i) + d0));
+            }
+        }
+        const float nm = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+        const float bs = nm == -INFINITY ? 0.f : nm, f0 = ex2(M - bs);
+        M = nm;
+        L *= f0;
+        O.x *= f0;
+        O.y *= f0;
+        O.z *= f0;
+        O.w *= f0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float f = ex2(ml[k].x - bs);
+            L = fmaf(f, ml[k].y, L);
+            O.x = fmaf(f, v[k].x, O.x);
+            O.y = fmaf(f, v[k].y, O.y);
+            O.z = fmaf(f, v[k].z, O.z);
+            O.w = fmaf(f, v[k].w, O.w);
+        }
     }
     so[grp][tid % TPR] = O;
-    if (tid % TPR == 0) sl[grp] = L;
+    if (tid % TPR == 0) sl[grp] = make_float2(M, L);
+    if (tid == 0) bad_row = 0;
     __syncthreads();
     const int hq = rec.h * p.G + row % p.G, tok = it.t0 + row / p.G;
     if (grp == 0) {
-        for (int k = 1; k < GR; ++k) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < GR; ++k) top = fmaxf(top, sl[k].x);
+        const float bs = top == -INFINITY ? 0.f : top;
+        O = make_float4(0.f, 0.f, 0.f, 0.f);
+        L = 0.f;
+#pragma unroll
+        for (int k = 0; k < GR; ++k) {
+            const float f = ex2(sl[k].x - bs);
             const float4 v = so[k][tid];
-            O.x += v.x;
-            O.y += v.y;
-            O.z += v.z;
-            O.w += v.w;
-            L += sl[k];
+            L = fmaf(f, sl[k].y, L);
+            O.x = fmaf(f, v.x, O.x);
+            O.y = fmaf(f, v.y, O.y);
+            O.z = fmaf(f, v.z, O.z);
+            O.w = fmaf(f, v.w, O.w);
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
         *reinterpret_cast<uint2 *>(p.out + tok * p.o_t + hq * p.o_h + d0) =
@@ -605,7 +729,7 @@ __global__ void __launch_bounds__(kThr) join_kernel(const __grid_constant__ Attn
 
 // ------------------------------------------------------------------ host side
 size_t stream_ws_bytes(int sms, int d) {
-    return (size_t)sms * kCtasPerSm * (sizeof(JoinRec) + (size_t)2 * 16 * (d + 4) * 4);
+    return (size_t)sms * ctas_per_sm(true) * (sizeof(JoinRec) + (size_t)2 * 16 * (d + 4) * 4);
 }
 
 template <int D, bool I8, int RT>
@@ -628,7 +752,7 @@ static cudaError_t launch(const AttnParams &p, cudaStream_t st) {
 
 cudaError_t stream_launch(const AttnParams &p0, int sms, cudaStream_t st) {
     AttnParams p = p0;
-    p.ctas = sms * kCtasPerSm;
+    p.ctas = sms * ctas_per_sm(p.c.i8);
     const bool small = p.max_tokens * p.G <= 8;
     if (p.c.d == 64) {
         if (p.c.i8) return small ? launch<64, true, 8>(p, st) : launch<64, true, 16>(p, st);

@@ -489,7 +489,7 @@ tiles_status_t check_desc(const tiles_paged_desc &d) {
     if (d.head_dim != 64 && d.head_dim != 128) return TILES_ERR_UNSUPPORTED;
     if (d.page_size != 16 && d.page_size != 32 && d.page_size != 64 && d.page_size != 128) return TILES_ERR_UNSUPPORTED;
     const long long lim = 0x7FFFFFFFll;
-    if ((long long)d.n_pages * d.n_kv_heads > lim / d.n_layers || (long long)d.table_width * d.page_size > lim / 4 ||
+    if ((long long)d.n_pages * d.n_kv_heads > lim / d.n_layers || (long long)d.n_pages * d.n_kv_heads > lim / (d.page_size / 16) || (long long)d.table_width * d.page_size > lim / 4 ||
         (long long)d.n_seqs * d.n_kv_heads > lim / 16)
         return TILES_ERR_UNSUPPORTED;
     return TILES_OK;
