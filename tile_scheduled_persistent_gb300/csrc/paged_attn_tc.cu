@@ -605,9 +605,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                                     f = __ldg(scales + ((size_t)pg * c.nkv + hh) * c.ps + (r & (c.ps - 1)));
                                 scale[kv][kb % kMaskRing][r] = f;
                             }
-#pragma unroll 1
-                            for (int k0 = 0; k0 < STEPS; k0 += AT_ONCE) {
-                                uint4 w4[AT_ONCE];
+                            auto load = [&](int k0, uint4 (&w4)[AT_ONCE]) {
 #pragma unroll
                                 for (int k = 0; k < AT_ONCE; ++k) {
                                     const int i = lt + S::LOADERS * (k0 + k), row = i / UPR, u = i % UPR;
@@ -617,10 +615,16 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                                         w4[k] = __ldg(reinterpret_cast<const uint4 *>(
                                             pool + (((size_t)pg * c.nkv + hh) * c.ps + (row & (c.ps - 1))) * D + 16 * u));
                                 }
+                            };
+                            uint4 now[AT_ONCE], next[AT_ONCE];
+                            load(0, now);
+#pragma unroll 1
+                            for (int k0 = 0; k0 < STEPS; k0 += AT_ONCE) {
+                                if (k0 + AT_ONCE < STEPS) load(k0 + AT_ONCE, next);
 #pragma unroll
                                 for (int k = 0; k < AT_ONCE; ++k) {
                                     const int i = lt + S::LOADERS * (k0 + k), row = i / UPR, u = i % UPR;
-                                    const uint32_t x[4] = {w4[k].x, w4[k].y, w4[k].z, w4[k].w};
+                                    const uint32_t x[4] = {now[k].x, now[k].y, now[k].z, now[k].w};
                                     uint32_t y[8];
 #pragma unroll
                                     for (int j = 0; j < 4; ++j) codes_bf16x2(x[j], y[2 * j], y[2 * j + 1]);
@@ -630,6 +634,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                                         *reinterpret_cast<uint4 *>(dst + (uu / 8) * S::HALF + row * 128 + (((uu % 8) ^ (row & 7)) << 4)) =
                                             make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
                                     }
+                                    now[k] = next[k];
                                 }
                             }
                             fence_proxy_async_smem();

@@ -21,14 +21,15 @@ namespace paged {
 
 constexpr int kBookThreads = 1024;
 constexpr int kMoveThreads = 256;
+constexpr int kRowsShared = 2048;  // rows whose first slot and length resize keeps in shared memory
 
 // Words that other threads of the kernel change: read at L2.
 __device__ __forceinline__ int ldw(const int32_t *p) { return __ldcg(p); }
 
 struct Book {
-    int32_t *status, *copies, *refs, *writers, *lowest, *src, *dst, *freelist, *need;
+    int32_t *status, *copies, *refs, *writers, *lowest, *src, *dst, *freelist, *first, *kinds;
 };
-__host__ __device__ __forceinline__ Book book_of(int32_t *state, int P) {
+__host__ __device__ __forceinline__ Book book_of(int32_t *state, int P, int n_seqs) {
     Book b;
     b.status = state + kStateStatus;
     b.copies = state + kStateCopies;
@@ -38,7 +39,8 @@ __host__ __device__ __forceinline__ Book book_of(int32_t *state, int P) {
     b.src = b.refs + 3 * (size_t)P;
     b.dst = b.refs + 4 * (size_t)P;
     b.freelist = b.refs + 5 * (size_t)P;
-    b.need = b.refs + 6 * (size_t)P;
+    b.first = b.refs + kStateArrays * (size_t)P;
+    b.kinds = b.first + n_seqs;
     return b;
 }
 
@@ -69,21 +71,25 @@ __device__ __forceinline__ int block_excl(int v, int *warps, int *total) {
 }
 
 // ------------------------------------------------------------------ resize
-// One CTA; a warp takes one row at a time. Steps, with a barrier between them:
-//   1. rows that shrink drop their pages (reference counts go down);
-//   2. pages that growing rows will write and that are shared: count the
-//      writers and find the lowest row among them, then settle who keeps the
-//      page (the lowest row, if every holder writes);
-//   3. pages needed per row, summed over rows in order;
-//   4. the lowest free pages, as many as needed;
-//   5. hand them out in order, and list the pages whose contents move.
-// A step reads what the one before it wrote, so reference counts and table
-// words go through L2.
+// One CTA, in steps with a barrier between them:
+//   1. rows that shrink drop their pages, a warp a row (reference counts go down);
+//   2. the pages that growing rows will write ("slots": row s, table entry j) are
+//      numbered in order; from here on a thread takes a slot;
+//   3. slots whose page is shared: count the page's writers and find the lowest
+//      row among them, which keeps the page if every holder writes;
+//   4. the slots that need a page, numbered in order;
+//   5. the lowest free pages, as many as needed;
+//   6. they are handed out in order, and the pages whose contents move are listed.
+// What bounds it is the chain of dependent L2 accesses (a step reads what the one
+// before it wrote, so counts and table words go through L2), hence a slot a thread
+// with its page, count and decision in registers. More than kBookThreads slots
+// take further rounds, whose decisions wait in memory (kinds).
 __global__ void __launch_bounds__(kBookThreads) resize_kernel(View c, const int32_t *__restrict__ new_lens) {
-    __shared__ int warps[32];
+    __shared__ int warps[32], first_s[kRowsShared], len_s[kRowsShared];
     __shared__ int n_copies;
-    const Book b = book_of(c.state, c.n_pages);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = kBookThreads / 32;
+    const Book b = book_of(c.state, c.n_pages, c.n_seqs);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool shared = c.n_seqs <= kRowsShared;
     const int P = c.n_pages, W = c.width, ps = c.ps;
     uint32_t flags = 0;
     if (tid == 0) n_copies = 0;
@@ -99,12 +105,27 @@ __global__ void __launch_bounds__(kBookThreads) resize_kernel(View c, const int3
         *nl = n < 0 ? *len : n;
     };
 
-    for (int s = warp; s < c.n_seqs; s += nw) {
-        int len, nl;
-        row(s, &len, &nl);
-        int32_t *t = c.tables + (size_t)s * W;
-        if (nl < len) {
-            for (int j = (nl + ps - 1) / ps + lane; j < W; j += 32) {
+    // 1, 2: a thread a row, then a warp a row that shrinks
+    long long slots = 0;
+    for (int s0 = 0; s0 < c.n_seqs; s0 += kBookThreads) {
+        const int s = s0 + tid;
+        int len = 0, nl = 0;
+        if (s < c.n_seqs) row(s, &len, &nl);
+        const int mine = nl > len ? ((nl + ps - 1) >> c.psl) - (len >> c.psl) : 0;
+        int sum;
+        const int before = block_excl(mine, warps, &sum);
+        if (s < c.n_seqs && shared) {
+            first_s[s] = (int)slots + before;
+            len_s[s] = len;
+        } else if (s < c.n_seqs) {
+            b.first[s] = (int)slots + before;
+        }
+        slots += sum;
+        for (uint32_t m = __ballot_sync(0xFFFFFFFFu, nl < len); m; m &= m - 1) {
+            const int src = __ffs(m) - 1, r = s0 + 32 * warp + src;
+            const int keep = __shfl_sync(0xFFFFFFFFu, nl, src);
+            int32_t *t = c.tables + (size_t)r * W;
+            for (int j = ((keep + ps - 1) >> c.psl) + lane; j < W; j += 32) {
                 const int page = t[j];
                 if (page == -1) continue;
                 if (page >= 0 && page < P)
@@ -113,76 +134,85 @@ __global__ void __launch_bounds__(kBookThreads) resize_kernel(View c, const int3
                     flags |= kDevBounds;
                 t[j] = -1;
             }
-            __syncwarp();
-            if (lane == 0) c.lens[s] = nl;
-        } else if (nl > len) {
-            for (int j = len / ps + lane; j < (nl + ps - 1) / ps; j += 32) {
-                const int page = t[j];
-                if (page >= 0 && page < P) {
-                    b.writers[page] = 0;  // the same words from every writer
-                    b.lowest[page] = 0x7FFFFFFF;
-                }
-            }
+            if (lane == 0) c.lens[r] = keep;
         }
     }
     __syncthreads();
-    for (int s = warp; s < c.n_seqs; s += nw) {
-        int len, nl;
-        row(s, &len, &nl);
-        const int32_t *t = c.tables + (size_t)s * W;
-        if (nl > len)
-            for (int j = len / ps + lane; j < (nl + ps - 1) / ps; j += 32) {
-                const int page = ldw(t + j);
-                if (page >= 0 && page < P && ldw(b.refs + page) > 1) {
-                    atomicAdd(b.writers + page, 1);
-                    atomicMin(b.lowest + page, s);
-                }
+    const int C = (int)slots;  // at most n_seqs * W
+    // slot k's row: the last with first[s] <= k (rows without slots share the next row's first)
+    auto first_of = [&](int s) { return shared ? first_s[s] : ldw(b.first + s); };
+    auto row_of = [&](int k) {
+        int lo = 0, n = c.n_seqs;
+        while (n > 1) {
+            const int h = n / 2;
+            if (first_of(lo + h) <= k) {
+                lo += h;
+                n -= h;
+            } else {
+                n = h;
             }
-    }
-    __syncthreads();
-    // a page with a holder that does not grow has no keeper (lowest = no row)
-    for (int s = warp; s < c.n_seqs; s += nw) {
-        int len, nl;
-        row(s, &len, &nl);
-        const int32_t *t = c.tables + (size_t)s * W;
-        if (nl > len)
-            for (int j = len / ps + lane; j < (nl + ps - 1) / ps; j += 32) {
-                const int page = ldw(t + j);
-                if (page >= 0 && page < P) {
-                    const int w = ldw(b.writers + page);
-                    if (w > 0 && w < ldw(b.refs + page)) atomicExch(b.lowest + page, -1);
-                }
-            }
-    }
-    __syncthreads();
-    // 0: has its own page, 1: needs one, 2: needs one in place of a shared one
-    auto kind = [&](int s, int page) {
-        if (page < 0 || page >= P) return 1;
-        return ldw(b.writers + page) > 0 && ldw(b.lowest + page) != s ? 2 : 0;
+        }
+        return lo;
     };
-    for (int s = warp; s < c.n_seqs; s += nw) {
-        int len, nl;
-        row(s, &len, &nl);
-        const int32_t *t = c.tables + (size_t)s * W;
-        int need = 0;
-        if (nl > len)
-            for (int j0 = len / ps; j0 < (nl + ps - 1) / ps; j0 += 32) {
-                const int j = j0 + lane;
-                need += __popc(__ballot_sync(0xFFFFFFFFu, j < (nl + ps - 1) / ps && kind(s, ldw(t + j)) != 0));
-            }
-        if (lane == 0) b.need[s] = need;
+    int my_s = 0, my_j = 0, my_len = 0, my_page = -1, my_ref = 0, my_kind = 0;  // of the first round's slot
+    auto slot = [&](int k, int *s, int *j, int *len, int *page, int *ref) {
+        *s = row_of(k);
+        *len = shared ? len_s[*s] : ldw(c.lens + *s);
+        *j = (*len >> c.psl) + k - first_of(*s);
+        *page = ldw(c.tables + (size_t)*s * W + *j);
+        *ref = *page >= 0 && *page < P ? ldw(b.refs + *page) : 0;
+    };
+    // 3
+    for (int k = tid; k < C; k += kBookThreads) {
+        int s, j, len, page, ref;
+        slot(k, &s, &j, &len, &page, &ref);
+        if (ref > 1) {
+            b.writers[page] = 0;  // the same words from every writer
+            b.lowest[page] = 0x7FFFFFFF;
+        }
+        if (k == tid) {
+            my_s = s;
+            my_j = j;
+            my_len = len;
+            my_page = page;
+            my_ref = ref;
+        }
     }
     __syncthreads();
-    int total = 0;
-    for (int s0 = 0; s0 < c.n_seqs; s0 += kBookThreads) {
-        const int s = s0 + tid;
-        int sum;
-        const int before = block_excl(s < c.n_seqs ? ldw(b.need + s) : 0, warps, &sum);
-        if (s < c.n_seqs) b.need[s] = total + before;
-        total += sum;
+    for (int k = tid; k < C; k += kBookThreads) {
+        int s = my_s, j = my_j, len = my_len, page = my_page, ref = my_ref;
+        if (k != tid) slot(k, &s, &j, &len, &page, &ref);
+        if (ref > 1) {
+            atomicAdd(b.writers + page, 1);
+            atomicMin(b.lowest + page, s);
+        }
     }
+    __syncthreads();
+    // 4. kinds: 0 has its own page, 1 needs one, 2 needs one in place of a shared one
+    int need = 0, my_rank = 0;
+    for (int k0 = 0; k0 < C; k0 += kBookThreads) {
+        const int k = k0 + tid;
+        int kind = 0;
+        if (k < C) {
+            int s = my_s, j = my_j, len = my_len, page = my_page, ref = my_ref;
+            if (k0) slot(k, &s, &j, &len, &page, &ref);
+            if (page < 0 || page >= P)
+                kind = 1;
+            else if (ref > 1)
+                kind = ldw(b.writers + page) == ref && ldw(b.lowest + page) == s ? 0 : 2;
+            if (k0)
+                b.kinds[k] = kind;
+            else
+                my_kind = kind;
+        }
+        int sum;
+        const int before = block_excl(kind != 0, warps, &sum);
+        if (k0 == 0) my_rank = before;
+        need += sum;
+    }
+    // 5
     int found = 0;
-    for (int p0 = 0; p0 < P && found < total; p0 += 4 * kBookThreads) {
+    for (int p0 = 0; p0 < P && found < need; p0 += 4 * kBookThreads) {
         const int p = p0 + 4 * tid;
         bool fr[4];
         int n = 0;
@@ -199,39 +229,45 @@ __global__ void __launch_bounds__(kBookThreads) resize_kernel(View c, const int3
         found += sum;
     }
     __syncthreads();
-    if (found < total) {
+    // 6
+    if (found < need) {
         flags |= kDevNoPages;
     } else {
-        for (int s = warp; s < c.n_seqs; s += nw) {
+        int given = 0;
+        for (int k0 = 0; k0 < C; k0 += kBookThreads) {
+            const int k = k0 + tid;
+            int s = my_s, j = my_j, len = my_len, page = my_page, ref, kind = my_kind, rank = my_rank;
+            if (k0) {
+                kind = 0;
+                if (k < C) {
+                    slot(k, &s, &j, &len, &page, &ref);
+                    kind = ldw(b.kinds + k);
+                }
+                int sum;
+                rank = given + block_excl(kind != 0, warps, &sum);
+                given += sum;
+            } else if (C > kBookThreads) {
+                block_excl(kind != 0, warps, &given);
+            }
+            if (k >= C || kind == 0) continue;
+            if (kind == 1 && page != -1) flags |= kDevBounds;
+            const int fresh = ldw(b.freelist + rank);
+            c.tables[(size_t)s * W + j] = fresh;
+            b.refs[fresh] = 1;
+            if (kind == 2) {
+                atomicSub(b.refs + page, 1);
+                if ((long long)j * ps < len) {
+                    const int i = atomicAdd(&n_copies, 1);
+                    b.src[i] = page;
+                    b.dst[i] = fresh;
+                }
+            }
+        }
+        __syncthreads();  // the lengths have been read
+        for (int s = tid; s < c.n_seqs; s += kBookThreads) {
             int len, nl;
             row(s, &len, &nl);
-            int32_t *t = c.tables + (size_t)s * W;
-            if (nl <= len) continue;
-            int at = ldw(b.need + s);
-            for (int j0 = len / ps; j0 < (nl + ps - 1) / ps; j0 += 32) {
-                const int j = j0 + lane;
-                const bool in = j < (nl + ps - 1) / ps;
-                const int page = in ? ldw(t + j) : 0;
-                const int k = in ? kind(s, page) : 0;
-                if (in && k == 1 && page != -1) flags |= kDevBounds;
-                const uint32_t m = __ballot_sync(0xFFFFFFFFu, k != 0);
-                if (k) {
-                    const int fresh = ldw(b.freelist + at + __popc(m & ((1u << lane) - 1u)));
-                    t[j] = fresh;
-                    b.refs[fresh] = 1;
-                    if (k == 2) {
-                        atomicSub(b.refs + page, 1);
-                        if ((long long)j * ps < len) {
-                            const int i = atomicAdd(&n_copies, 1);
-                            b.src[i] = page;
-                            b.dst[i] = fresh;
-                        }
-                    }
-                }
-                at += __popc(m);
-            }
-            __syncwarp();
-            if (lane == 0) c.lens[s] = nl;
+            if (nl > len) c.lens[s] = nl;
         }
     }
     if (flags) atomicOr(reinterpret_cast<uint32_t *>(b.status), flags);
@@ -260,7 +296,8 @@ __device__ __forceinline__ void move_bytes(const uint8_t *src, uint8_t *dst, lon
 }
 
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(View c, int remap) {
-    const Book b = book_of(c.state, c.n_pages);
+    const Book b = book_of(c.state, c.n_pages, c.n_seqs);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int n = *b.copies;
     const long long block = (long long)c.nkv * c.ps * c.d * (c.i8 ? 1 : 2), scales = (long long)c.nkv * c.ps * 4;
     // one work item: a page of one layer of K or of V
@@ -296,7 +333,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(View c, int remap) {
 // ------------------------------------------------------------------ fork
 // One warp per row.
 __global__ void __launch_bounds__(32) fork_kernel(View c, const int32_t *__restrict__ src_rows) {
-    const Book b = book_of(c.state, c.n_pages);
+    const Book b = book_of(c.state, c.n_pages, c.n_seqs);
     const int s = blockIdx.x, lane = threadIdx.x, W = c.width;
     const int from = src_rows[s];
     if (from < 0) return;
@@ -333,7 +370,7 @@ __global__ void __launch_bounds__(32) fork_kernel(View c, const int32_t *__restr
 // One warp per row: pages that begin at or behind `sinks` and end at or before
 // position len - window.
 __global__ void __launch_bounds__(32) trim_kernel(View c, int window, int sinks) {
-    const Book b = book_of(c.state, c.n_pages);
+    const Book b = book_of(c.state, c.n_pages, c.n_seqs);
     const int s = blockIdx.x, lane = threadIdx.x, ps = c.ps;
     int len = c.lens[s];
     if (len > c.width * ps) len = c.width * ps;
@@ -356,7 +393,7 @@ __global__ void __launch_bounds__(32) trim_kernel(View c, int window, int sinks)
 // tables follow in move_kernel.
 __global__ void __launch_bounds__(kBookThreads) compact_kernel(View c) {
     __shared__ int warps[32];
-    const Book b = book_of(c.state, c.n_pages);
+    const Book b = book_of(c.state, c.n_pages, c.n_seqs);
     const int tid = threadIdx.x, P = c.n_pages;
     int live = 0, sum;
     for (int p = tid; p < P; p += kBookThreads) live += b.refs[p] > 0;
@@ -490,7 +527,7 @@ tiles_status_t check_desc(const tiles_paged_desc &d) {
     if (d.page_size != 16 && d.page_size != 32 && d.page_size != 64 && d.page_size != 128) return TILES_ERR_UNSUPPORTED;
     const long long lim = 0x7FFFFFFFll;
     if ((long long)d.n_pages * d.n_kv_heads > lim / d.n_layers || (long long)d.n_pages * d.n_kv_heads > lim / (d.page_size / 16) || (long long)d.table_width * d.page_size > lim / 4 ||
-        (long long)d.n_seqs * d.n_kv_heads > lim / 16)
+        (long long)d.n_seqs * d.n_kv_heads > lim / 16 || (long long)d.n_seqs * d.table_width > lim)
         return TILES_ERR_UNSUPPORTED;
     return TILES_OK;
 }
@@ -504,7 +541,7 @@ void layout_of(const tiles_paged_desc &d, tiles_paged_layout *o) {
         o->k_scale_off = o->v_scale_off = 0;
         o->k_bytes = o->v_bytes = rows * d.head_dim * 2;
     }
-    o->state_bytes = 4 * ((int64_t)kStateRefs + (int64_t)kStateArrays * d.n_pages + d.n_seqs);
+    o->state_bytes = 4 * ((int64_t)kStateRefs + (int64_t)kStateArrays * d.n_pages + d.n_seqs + (int64_t)d.n_seqs * d.table_width);
 }
 
 tiles_status_t check_cache(const tiles_paged_cache *c) {
@@ -562,6 +599,20 @@ int64_t attn_ws_bytes(const tiles_paged_desc &d, int n_q_heads, int max_tokens, 
                                                                   : tc_ws_bytes(sms, d.head_dim));
 }
 
+// The kernel that moves the pages, set up while the one that lists them runs.
+tiles_status_t launch_move(const View &v, int remap, int sms, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(sms * 8));
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, move_kernel, v, remap) == cudaSuccess ? TILES_OK : TILES_ERR_CUDA;
+}
+
 tiles_status_t launched() { return cudaGetLastError() == cudaSuccess ? TILES_OK : TILES_ERR_CUDA; }
 
 }  // namespace
@@ -598,8 +649,8 @@ tiles_status_t tiles_paged_resize(const tiles_paged_cache *cache, const int32_t 
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const View v = view_of(*cache, 0);
     resize_kernel<<<1, kBookThreads, 0, cs>>>(v, new_lens);
-    move_kernel<<<sms * 8, kMoveThreads, 0, cs>>>(v, 0);
-    return launched();
+    if ((st = launched()) != TILES_OK) return st;
+    return launch_move(v, 0, sms, cs);
 }
 
 tiles_status_t tiles_paged_fork(const tiles_paged_cache *cache, const int32_t *src_rows, void *stream) {
@@ -626,8 +677,8 @@ tiles_status_t tiles_paged_compact(const tiles_paged_cache *cache, void *stream)
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const View v = view_of(*cache, 0);
     compact_kernel<<<1, kBookThreads, 0, cs>>>(v);
-    move_kernel<<<sms * 8, kMoveThreads, 0, cs>>>(v, 1);
-    return launched();
+    if ((st = launched()) != TILES_OK) return st;
+    return launch_move(v, 1, sms, cs);
 }
 
 tiles_status_t tiles_paged_append(const tiles_paged_cache *cache, int32_t layer, const void *k, int64_t k_stride_token,

@@ -17,7 +17,8 @@ namespace paged {
 
 // int32 words of the state buffer: the status word, then (at kStateRefs) the
 // reference counts and working memory of n_pages words each (writers, lowest,
-// copy sources, copy targets, free list), then n_seqs words (pages a row needs)
+// copy sources, copy targets, free list), then n_seqs words (each row's first slot)
+// and n_seqs table_width words (what slots need)
 constexpr int kStateStatus = 0, kStateCopies = 1, kStateRefs = 16;
 constexpr int kStateArrays = 6;
 
