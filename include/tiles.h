@@ -585,6 +585,26 @@ tiles_status_t tiles_paged_attention(const tiles_paged_cache *cache, int32_t lay
 tiles_status_t tiles_paged_workspace_bytes(const tiles_paged_desc *desc, int32_t n_q_heads, int32_t max_tokens,
                                            int64_t *bytes);
 
+/* The multi-token pass (tiles_forward) over a paged cache: one step of many
+ * sequences at once. The new tokens of row s are those of tiles_paged_append, at
+ * its last positions (tiles_paged_resize first); the pass appends their K and V
+ * in every layer and attends within `window` and `sinks` (tiles_paged_attention).
+ * One token a row decodes a batch; many tokens of one row are a piece of its
+ * prompt or a verify step; both can stand in one pass.
+ *   tokens      device, n_tokens <= TILES_MAX_FORWARD_TOKENS ids in [0, vocab)
+ *   out_argmax  device, n_tokens int32: the greedy token after each input
+ *   out_logits  device, [n_tokens][vocab] float32, or NULL
+ * What comes out for tokens without a position (padding, positions below 0) is
+ * undefined; their ids must be in range. A position >= the plan's max_pos and an
+ * id out of range are recorded in the plan's status word (tiles_status), the
+ * cache's faults in its own. The cache has the plan's n_layers, n_kv_heads and
+ * head_dim, in either format; BF16 weights only. The first call allocates the
+ * plan's working memory for these passes. Errors: INVALID_ARG, UNSUPPORTED,
+ * DEVICE_MISMATCH, CUDA. */
+tiles_status_t tiles_forward_paged(tiles_plan_t plan, const tiles_paged_cache *cache, const int32_t *tokens,
+                                   int32_t n_tokens, const int32_t *cu_tokens, int32_t max_tokens, int32_t window,
+                                   int32_t sinks, void *stream, int32_t *out_argmax, float *out_logits);
+
 /* Synchronises `stream`, reads the cache's status word and clears it: TILES_OK,
  * TILES_ERR_DEVICE_BOUNDS, TILES_ERR_CAPACITY, TILES_ERR_TIMEOUT or CUDA. */
 tiles_status_t tiles_paged_status(const tiles_paged_cache *cache, void *stream);

@@ -129,7 +129,7 @@ EXPORTS = ("tiles_plan_create", "tiles_plan_destroy", "tiles_decode", "tiles_dec
            "tiles_forward", "tiles_verify", "tiles_kv8_get_layout", "tiles_kv8_from_bf16",
            "tiles_paged_get_layout", "tiles_paged_reset", "tiles_paged_resize", "tiles_paged_fork",
            "tiles_paged_trim", "tiles_paged_compact", "tiles_paged_append", "tiles_paged_attention",
-           "tiles_paged_workspace_bytes", "tiles_paged_status")
+           "tiles_paged_workspace_bytes", "tiles_paged_status", "tiles_forward_paged")
 MAX_FORWARD_TOKENS = 256
 
 _lib_handle = None
@@ -203,6 +203,8 @@ def _lib():
                                             vp, i64, vp]
         L.tiles_paged_workspace_bytes.argtypes = [ctypes.POINTER(PagedDesc), i32, i32, ctypes.POINTER(i64)]
         L.tiles_paged_status.argtypes = [pc, vp]
+        L.tiles_forward_paged.argtypes = [vp, pc, vp, i32, vp, i32, i32, i32, vp, vp, vp]
+        L.tiles_forward_paged.restype = st
         for n in EXPORTS:
             if n.startswith("tiles_paged_"):
                 getattr(L, n).restype = st
@@ -626,6 +628,16 @@ class Plan:
         _check(_lib().tiles_forward(self._h, _ptr(k_cache), _ptr(v_cache), _ptr(tokens),
                                     int(tokens.numel()), start_pos, _stream_ptr(stream),
                                     _ptr(out_argmax), _ptr(out_logits)), "tiles_forward")
+
+    def forward_paged(self, cache: PagedKV, tokens, out_argmax, cu_tokens=None, max_tokens: int = 1,
+                      window: int = 0, sinks: int = 0, out_logits=None, stream=None) -> None:
+        """One pass over a paged cache: the int32 CUDA tensor `tokens` (up to MAX_FORWARD_TOKENS) holds
+        the new tokens of the cache's rows, row s those from cu_tokens[s] on (None: one a row), at the
+        rows' last positions (``cache.resize`` first). Their K/V rows are appended; out_argmax int32 [n]
+        gets the greedy token after each, out_logits float32 [n][vocab] (or None) the logits."""
+        _check(_lib().tiles_forward_paged(self._h, cache._ref, _ptr(tokens), int(tokens.numel()),
+                                          cache._cu(cu_tokens, "tiles_forward_paged"), max_tokens, window, sinks,
+                                          cache._on(stream), _ptr(out_argmax), _ptr(out_logits)), "tiles_forward_paged")
 
     def verify(self, k_cache, v_cache, inputs, start_pos: int, out_tokens, out_n_accepted,
                out_logits=None, stream=None) -> None:

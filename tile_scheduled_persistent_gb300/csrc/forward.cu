@@ -28,6 +28,7 @@
 #include <vector>
 
 #include "megakernel.cuh"
+#include "paged_internal.h"
 #include "plan_internal.h"
 
 namespace tiles {
@@ -174,13 +175,16 @@ __global__ void __launch_bounds__(256) swiglu_kernel(const float *__restrict__ p
 // Per token and head (grid T x (nq + 2 nkv), one warp each, D / 32 elements a
 // lane): the split sums of the Q/K/V rows, per-head RMSNorm (q_norm / k_norm)
 // when enabled, RoPE at position P0 + t, q -> the q buffer (bf16), k and v ->
-// the caches at P0 + t (bf16).
-template <int D>
+// the caches at P0 + t (bf16). PAGED: token t is at position pos[t] of a sequence
+// of its own, and kc / vc are rows [T][nkv][D] to be appended to its pages
+// (max_pos = 1, layer 0; a token without a position, pos[t] < 0, takes part as if
+// at 0: nothing reads its rows).
+template <int D, bool PAGED = false>
 __global__ void __launch_bounds__(32) qkv_post_kernel(const float *part, int sk, int T, int rows, int nq, int nkv,
                                                       int max_pos, int layer, int P0, int qk_norm, float eps,
                                                       const uint16_t *q_norm, const uint16_t *k_norm,
                                                       const float *rope_cos, const float *rope_sin, uint16_t *q,
-                                                      uint16_t *kc, uint16_t *vc) {
+                                                      uint16_t *kc, uint16_t *vc, const int32_t *pos = nullptr) {
     constexpr int E = D / 32;
     const int t = blockIdx.x, hh = blockIdx.y, lane = threadIdx.x;
     const bool is_q = hh < nq, is_k = !is_q && hh < nq + nkv;
@@ -205,8 +209,8 @@ __global__ void __launch_bounds__(32) qkv_post_kernel(const float *part, int sk,
     for (; s < sk; ++s)
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = __fadd_rn(v[e], __ldg(pt + (size_t)s * zs + 32 * e));
-    const int P = P0 + t;
-    const size_t crow = (((size_t)layer * nkv + kvh) * max_pos + P) * D;
+    const int P = PAGED ? max(0, pos[t]) : P0 + t;
+    const size_t crow = (PAGED ? (size_t)t * nkv + kvh : ((size_t)layer * nkv + kvh) * max_pos + P) * D;
     if (!is_q && !is_k) {
 #pragma unroll
         for (int e = 0; e < E; ++e) vc[crow + lane + 32 * e] = f2bf(v[e]);
@@ -574,9 +578,17 @@ tiles_status_t forward_setup(tiles_plan_s *plan) {
     return TILES_OK;
 }
 
-// One pass of T <= kMaxTokens tokens at positions P0 .. P0 + T - 1.
+// What a pass over a paged cache has in the place of the dense caches.
+struct PagedPass {
+    const tiles_paged_cache *cache;
+    const int32_t *cu;
+    int max_tokens, window, sinks;
+};
+
+// One pass of T <= kMaxTokens tokens: at positions P0 .. P0 + T - 1 of the dense
+// caches kc, vc, or (pg) at their places in the sequences of a paged cache.
 tiles_status_t forward_pass(tiles_plan_s *plan, uint16_t *kc, uint16_t *vc, const int32_t *tokens, int T, int P0,
-                            cudaStream_t st, int32_t *argmax, float *logits) {
+                            cudaStream_t st, int32_t *argmax, float *logits, const PagedPass *pg = nullptr) {
     const Geom &g = plan->sched.geom;
     const KernelParams &kp = plan->base;
     ForwardScratch &f = plan->fwd;
@@ -587,14 +599,33 @@ tiles_status_t forward_pass(tiles_plan_s *plan, uint16_t *kc, uint16_t *vc, cons
     embed_norm_kernel<<<T, 256, 0, st>>>(tokens, kp.embed, g.V, g.H, lp[0].attn_norm, eps, f.x, f.h, kp.status);
     const int split = attn_split_len(g, P0, T, sms);
     const int S = (P0 + T + split - 1) / split;
-    if ((size_t)T * S > f.attn_pairs) return TILES_ERR_CAPACITY;
+    if (!pg && (size_t)T * S > f.attn_pairs) return TILES_ERR_CAPACITY;
+    if (pg) {
+        const cudaError_t pe = paged::positions_launch(*pg->cache, pg->cu, T, g.max_pos, f.pos, kp.status, st);
+        if (pe != cudaSuccess) return TILES_ERR_CUDA;
+    }
     const dim3 agrid((T * g.G + 63) / 64, g.nkv, S);
     for (int l = 0; l < g.L; ++l) {
         const LayerPtrs &L = lp[l];
         if (gemm(plan, L.qkv, g.H, f.h, g.H, g.qkv_rows, T, g.H, f.part, 1 << 30, &sk, st) != cudaSuccess)
             return TILES_ERR_CUDA;
         const dim3 qgrid(T, g.nq + 2 * g.nkv);
-        if (g.d == 64)
+        if (pg) {
+            uint16_t *kr = f.kv_rows, *vr = f.kv_rows + (size_t)T * g.kvd;
+            if (g.d == 64)
+                qkv_post_kernel<64, true><<<qgrid, 32, 0, st>>>(f.part, sk, T, g.qkv_rows, g.nq, g.nkv, 1, 0, 0, kp.qk_norm,
+                                                                eps, L.q_norm, L.k_norm, kp.rope_cos, kp.rope_sin, f.q,
+                                                                kr, vr, f.pos);
+            else
+                qkv_post_kernel<128, true><<<qgrid, 32, 0, st>>>(f.part, sk, T, g.qkv_rows, g.nq, g.nkv, 1, 0, 0, kp.qk_norm,
+                                                                 eps, L.q_norm, L.k_norm, kp.rope_cos, kp.rope_sin, f.q,
+                                                                 kr, vr, f.pos);
+            tiles_status_t ps = tiles_paged_append(pg->cache, l, kr, g.kvd, g.d, vr, g.kvd, g.d, pg->cu, T, st);
+            if (ps == TILES_OK)
+                ps = tiles_paged_attention(pg->cache, l, g.nq, f.q, g.qd, g.d, f.o, g.qd, g.d, pg->cu, T, pg->max_tokens,
+                                           kp.attn_scale, pg->window, pg->sinks, f.paged_ws, (int64_t)f.paged_ws_bytes, st);
+            if (ps != TILES_OK) return ps;
+        } else if (g.d == 64)
             qkv_post_kernel<64><<<qgrid, 32, 0, st>>>(f.part, sk, T, g.qkv_rows, g.nq, g.nkv, g.max_pos, l, P0,
                                                       kp.qk_norm, eps, L.q_norm, L.k_norm, kp.rope_cos,
                                                       kp.rope_sin, f.q, kc, vc);
@@ -602,13 +633,14 @@ tiles_status_t forward_pass(tiles_plan_s *plan, uint16_t *kc, uint16_t *vc, cons
             qkv_post_kernel<128><<<qgrid, 32, 0, st>>>(f.part, sk, T, g.qkv_rows, g.nq, g.nkv, g.max_pos, l, P0,
                                                        kp.qk_norm, eps, L.q_norm, L.k_norm, kp.rope_cos,
                                                        kp.rope_sin, f.q, kc, vc);
-        if (g.d == 64)
+        if (pg) {
+        } else if (g.d == 64)
             attn_mt_kernel<64><<<agrid, 128, attn_smem(64), st>>>(f.q, kc, vc, l, g.nq, g.nkv, g.G, g.max_pos, P0, T, split,
                                                       kp.attn_scale, f.apart, S);
         else
             attn_mt_kernel<128><<<agrid, 128, attn_smem(128), st>>>(f.q, kc, vc, l, g.nq, g.nkv, g.G, g.max_pos, P0, T, split,
                                                        kp.attn_scale, f.apart, S);
-        attn_combine_kernel<<<dim3(T, g.nq), g.d, 0, st>>>(f.apart, S, g.nq, g.d, f.o);
+        if (!pg) attn_combine_kernel<<<dim3(T, g.nq), g.d, 0, st>>>(f.apart, S, g.nq, g.d, f.o);
         if (gemm(plan, L.o, g.qd, f.o, g.qd, g.H, T, g.qd, f.part, 1 << 30, &sk, st) != cudaSuccess)
             return TILES_ERR_CUDA;
         resid_norm_kernel<<<T, 512, 0, st>>>(f.part, sk, T, g.H, f.x, L.ffn_norm, eps, f.h);
@@ -646,9 +678,46 @@ tiles_status_t forward_check(tiles_plan_t plan, void *k_cache, void *v_cache, in
     return forward_setup(plan);
 }
 
+// Working memory of passes over a paged cache (first use): the new K and V rows,
+// the tokens' positions, the attention's workspace for any number of tokens.
+tiles_status_t paged_setup(tiles_plan_s *plan) {
+    ForwardScratch &f = plan->fwd;
+    if (f.paged_ready) return TILES_OK;
+    const Geom &g = plan->sched.geom;
+    f.paged_ws_bytes = std::max(paged::stream_ws_bytes(plan->sm_count, g.d), paged::tc_ws_bytes(plan->sm_count, g.d));
+    uint8_t *ws;
+    if (falloc(plan, &f.kv_rows, (size_t)2 * kMaxTokens * g.kvd * 2) != cudaSuccess ||
+        falloc(plan, &f.pos, (size_t)kMaxTokens * 4) != cudaSuccess || falloc(plan, &ws, f.paged_ws_bytes) != cudaSuccess)
+        return TILES_ERR_CUDA;
+    f.paged_ws = ws;
+    f.paged_ready = true;
+    return TILES_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+tiles_status_t tiles_forward_paged(tiles_plan_t plan, const tiles_paged_cache *cache, const int32_t *tokens,
+                                   int32_t n_tokens, const int32_t *cu_tokens, int32_t max_tokens, int32_t window,
+                                   int32_t sinks, void *stream, int32_t *out_argmax, float *out_logits) {
+    if (!plan || !cache || !tokens || !out_argmax || n_tokens < 1 || n_tokens > kMaxTokens || max_tokens < 1 || window < 0 ||
+        sinks < 0)
+        return TILES_ERR_INVALID_ARG;
+    tiles_status_t st = paged::cache_check(cache);
+    if (st != TILES_OK) return st;
+    const Geom &g = plan->sched.geom;
+    const tiles_paged_desc &d = cache->desc;
+    if (d.n_layers != g.L || d.n_kv_heads != g.nkv || d.head_dim != g.d || (!cu_tokens && n_tokens != d.n_seqs))
+        return TILES_ERR_INVALID_ARG;
+    if (g.wbytes != 2) return TILES_ERR_UNSUPPORTED;  // BF16 weights only
+    if ((st = plan_check_device(plan)) != TILES_OK || (st = forward_setup(plan)) != TILES_OK ||
+        (st = paged_setup(plan)) != TILES_OK)
+        return st;
+    const PagedPass pg = {cache, cu_tokens, std::min(max_tokens, n_tokens), window, sinks};
+    return forward_pass(plan, nullptr, nullptr, tokens, n_tokens, 0, reinterpret_cast<cudaStream_t>(stream), out_argmax,
+                        out_logits, &pg);
+}
 
 tiles_status_t tiles_forward(tiles_plan_t plan, void *k_cache, void *v_cache, const int32_t *tokens,
                              int32_t n_tokens, int32_t start_pos, void *stream, int32_t *out_argmax,

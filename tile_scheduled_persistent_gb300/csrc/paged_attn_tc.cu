@@ -62,17 +62,19 @@ struct TcShape {
     static constexpr int BLOCK = HALF * (D / 64);       // one block of K or V, or a query tile
     static constexpr int RING = D == 128 ? 4 : 8;
     // threads a query row's softmax is shared by
-    static constexpr int HALVES = D == 64 ? 1 : 2;
-    // warpgroups: HALVES of softmax for each tile; one of the MMA issuer, the loader (INT8: two
-    // warps) and the planner
-    static constexpr int SOFTMAX = 8 * HALVES, THREADS = (SOFTMAX + 4) * 32, LOADERS = I8 ? 64 : 32;
+    static constexpr int HALVES = D == 64 || I8 ? 1 : 2;
+    // warpgroups: HALVES of softmax for each tile; one of the MMA issuer, the loader and the
+    // planner; with an INT8 cache one of loaders, as widening takes four warps
+    static constexpr int SOFTMAX = 8 * HALVES, THREADS = (SOFTMAX + 4 + (I8 ? 4 : 0)) * 32, LOADERS = I8 ? 128 : 32;
+    static constexpr int LOADER = SOFTMAX + (I8 ? 4 : 1);  // its first warp
     // registers a thread after the split; the sums are the launch's: 2 x 208 + 88 = 3 x 168 of
-    // 384 threads, 4 x 104 + 64 = 5 x 96 of 640
-    static constexpr int REG_SOFTMAX = HALVES == 1 ? 208 : 104, REG_ISSUE = HALVES == 1 ? 88 : 64;
+    // 384 threads, 4 x 104 + 64 = 5 x 96 of 640, 2 x 184 + 56 + 88 = 4 x 128 of 512
+    static constexpr int REG_SOFTMAX = I8 ? 184 : HALVES == 1 ? 208 : 104, REG_ISSUE = I8 ? 56 : HALVES == 1 ? 88 : 64,
+                         REG_LOAD = 88;
     // tensor memory, 512 columns: scores of the two tiles (128 each), O (D each) and, at D 64,
     // room for the weights of their own; at D 128 they take the place of the scores
     static constexpr bool SPLIT = D == 64;
-    static constexpr int O_COL = 256, P_COL = SPLIT ? 384 : 0, P_TILE = SPLIT ? 64 : 128, P_HALF = SPLIT ? 32 : 64;
+    static constexpr int O_COL = 256, P_COL = SPLIT ? 384 : 0, P_TILE = SPLIT ? 64 : 128, P_HALF = HALVES == 1 ? 32 : 64;
     static constexpr int PART = kPair * (D + 2);        // floats of a partial state: o [D / 4][row][4], m [row], l [row]
     static constexpr int SCALES = I8 ? 2 * 16 * kBlock * 4 : 0;  // bytes: a block's K and V scales, by block number
 };
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
         };
         // ================================================ loader
         auto loader = [&]() {
-            const int lt = tid - (S::SOFTMAX + 1) * 32;  // thread of the loader
+            const int lt = tid - S::LOADER * 32;  // thread of the loader
             int n = 0;                     // blocks of K and V so far
             uint32_t kb = 0, fixes = 0;    // key blocks, repaired blocks so far
             for (uint32_t sk = 0; seg_begin(sk); ++sk) {
@@ -605,7 +607,9 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                                     f = __ldg(scales + ((size_t)pg * c.nkv + hh) * c.ps + (r & (c.ps - 1)));
                                 scale[kv][kb % kMaskRing][r] = f;
                             }
-                            auto load = [&](int k0, uint4 (&w4)[AT_ONCE]) {
+#pragma unroll 1
+                            for (int k0 = 0; k0 < STEPS; k0 += AT_ONCE) {
+                                uint4 w4[AT_ONCE];
 #pragma unroll
                                 for (int k = 0; k < AT_ONCE; ++k) {
                                     const int i = lt + S::LOADERS * (k0 + k), row = i / UPR, u = i % UPR;
@@ -615,16 +619,10 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                                         w4[k] = __ldg(reinterpret_cast<const uint4 *>(
                                             pool + (((size_t)pg * c.nkv + hh) * c.ps + (row & (c.ps - 1))) * D + 16 * u));
                                 }
-                            };
-                            uint4 now[AT_ONCE], next[AT_ONCE];
-                            load(0, now);
-#pragma unroll 1
-                            for (int k0 = 0; k0 < STEPS; k0 += AT_ONCE) {
-                                if (k0 + AT_ONCE < STEPS) load(k0 + AT_ONCE, next);
 #pragma unroll
                                 for (int k = 0; k < AT_ONCE; ++k) {
                                     const int i = lt + S::LOADERS * (k0 + k), row = i / UPR, u = i % UPR;
-                                    const uint32_t x[4] = {now[k].x, now[k].y, now[k].z, now[k].w};
+                                    const uint32_t x[4] = {w4[k].x, w4[k].y, w4[k].z, w4[k].w};
                                     uint32_t y[8];
 #pragma unroll
                                     for (int j = 0; j < 4; ++j) codes_bf16x2(x[j], y[2 * j], y[2 * j + 1]);
@@ -634,7 +632,6 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                                         *reinterpret_cast<uint4 *>(dst + (uu / 8) * S::HALF + row * 128 + (((uu % 8) ^ (row & 7)) << 4)) =
                                             make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
                                     }
-                                    now[k] = next[k];
                                 }
                             }
                             fence_proxy_async_smem();
@@ -733,13 +730,16 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             }
         };
         // ================================================ softmax, half a query row a thread
-        if (warp >= S::SOFTMAX) {
+        if (I8 && warp >= S::LOADER) {
+            regs_down<S::REG_LOAD>();
+            loader();
+        } else if (warp >= S::SOFTMAX) {
             regs_down<S::REG_ISSUE>();
             if (warp == S::SOFTMAX)
                 issuer();
             else if (warp == S::SOFTMAX + 3)
                 planner();
-            else if (I8 || warp == S::SOFTMAX + 1)
+            else if (!I8 && warp == S::LOADER)
                 loader();
         } else {
             regs_up<S::REG_SOFTMAX>();
@@ -1010,7 +1010,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             commit(&ctl->drain);
             bounded_wait(&ctl->drain, 0u, d2, &never);
         }
-        if (!I8 && warp == S::SOFTMAX + 1 && lane == 0)
+        if (!I8 && warp == S::LOADER && lane == 0)
             for (int k = max(0, issued - RING); k < issued; ++k)
                 bounded_wait(&ctl->full[k % RING], (uint32_t)(k / RING) & 1u, d2, &never);
     }

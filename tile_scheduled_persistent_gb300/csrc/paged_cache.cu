@@ -85,7 +85,7 @@ __device__ __forceinline__ int block_excl(int v, int *warps, int *total) {
 // with its page, count and decision in registers. More than kBookThreads slots
 // take further rounds, whose decisions wait in memory (kinds).
 __global__ void __launch_bounds__(kBookThreads) resize_kernel(View c, const int32_t *__restrict__ new_lens) {
-    __shared__ int warps[32], first_s[kRowsShared], len_s[kRowsShared];
+    __shared__ int warps[32], first_s[kRowsShared], len_s[kRowsShared], new_s[kRowsShared];
     __shared__ int n_copies;
     const Book b = book_of(c.state, c.n_pages, c.n_seqs);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kBookThreads) resize_kernel(View c, const int3
         *nl = n < 0 ? *len : n;
     };
 
-    // 1, 2: a thread a row, then a warp a row that shrinks
+    // 1, 2: a thread a row, then a warp each row that shrinks
     long long slots = 0;
     for (int s0 = 0; s0 < c.n_seqs; s0 += kBookThreads) {
         const int s = s0 + tid;
@@ -117,25 +117,34 @@ __global__ void __launch_bounds__(kBookThreads) resize_kernel(View c, const int3
         if (s < c.n_seqs && shared) {
             first_s[s] = (int)slots + before;
             len_s[s] = len;
+            new_s[s] = nl;
         } else if (s < c.n_seqs) {
             b.first[s] = (int)slots + before;
         }
         slots += sum;
-        for (uint32_t m = __ballot_sync(0xFFFFFFFFu, nl < len); m; m &= m - 1) {
-            const int src = __ffs(m) - 1, r = s0 + 32 * warp + src;
-            const int keep = __shfl_sync(0xFFFFFFFFu, nl, src);
-            int32_t *t = c.tables + (size_t)r * W;
-            for (int j = ((keep + ps - 1) >> c.psl) + lane; j < W; j += 32) {
-                const int page = t[j];
-                if (page == -1) continue;
-                if (page >= 0 && page < P)
-                    atomicSub(b.refs + page, 1);
-                else
-                    flags |= kDevBounds;
-                t[j] = -1;
-            }
-            if (lane == 0) c.lens[r] = keep;
+    }
+    __syncthreads();
+    for (int s = warp; s < c.n_seqs; s += kBookThreads / 32) {
+        int len, nl;
+        if (shared) {
+            len = len_s[s];
+            nl = new_s[s];
+        } else {
+            row(s, &len, &nl);
         }
+        if (nl >= len) continue;
+        int32_t *t = c.tables + (size_t)s * W;
+        for (int j = ((nl + ps - 1) >> c.psl) + lane; j < W; j += 32) {
+            const int page = t[j];
+            if (page == -1) continue;
+            if (page >= 0 && page < P)
+                atomicSub(b.refs + page, 1);
+            else
+                flags |= kDevBounds;
+            t[j] = -1;
+        }
+        __syncwarp();
+        if (lane == 0) c.lens[s] = nl;
     }
     __syncthreads();
     const int C = (int)slots;  // at most n_seqs * W
@@ -265,8 +274,13 @@ __global__ void __launch_bounds__(kBookThreads) resize_kernel(View c, const int3
         }
         __syncthreads();  // the lengths have been read
         for (int s = tid; s < c.n_seqs; s += kBookThreads) {
-            int len, nl;
-            row(s, &len, &nl);
+            int len = 0, nl = 0;
+            if (shared) {
+                len = len_s[s];
+                nl = new_s[s];
+            } else {
+                row(s, &len, &nl);
+            }
             if (nl > len) c.lens[s] = nl;
         }
     }
@@ -508,6 +522,32 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
     }
 }
 
+// One warp per token.
+__global__ void __launch_bounds__(32) positions_kernel(const int32_t *__restrict__ lens, int n_seqs,
+                                                       const int32_t *__restrict__ cu, int max_pos, int32_t *pos,
+                                                       uint32_t *status) {
+    const int t = blockIdx.x, lane = threadIdx.x;
+    int p = -1;
+    if (cu) {
+        const int s = row_of_token(cu, n_seqs, t, lane);
+        if (s >= 0) p = __ldg(lens + s) - __ldg(cu + s + 1) + t;
+    } else {
+        p = __ldg(lens + t) - 1;
+    }
+    if (lane) return;
+    if (p >= max_pos) {
+        atomicOr(status, kDevBounds);
+        p = -1;
+    }
+    pos[t] = p < 0 ? -1 : p;
+}
+
+cudaError_t positions_launch(const tiles_paged_cache &cache, const int32_t *cu, int n_tokens, int max_pos, int32_t *pos,
+                             uint32_t *status, cudaStream_t st) {
+    positions_kernel<<<n_tokens, 32, 0, st>>>(cache.lens, cache.desc.n_seqs, cu, max_pos, pos, status);
+    return cudaGetLastError();
+}
+
 }  // namespace paged
 }  // namespace tiles
 
@@ -553,6 +593,12 @@ tiles_status_t check_cache(const tiles_paged_cache *c) {
         return TILES_ERR_INVALID_ARG;
     return TILES_OK;
 }
+
+}  // namespace
+
+tiles_status_t tiles::paged::cache_check(const tiles_paged_cache *cache) { return check_cache(cache); }
+
+namespace {
 
 // The pools from `layer` on.
 View view_of(const tiles_paged_cache &c, int layer) {

@@ -97,6 +97,14 @@ __device__ __forceinline__ void visible_span(const AttnParams &p, int len, int f
     }
 }
 
+// The host-side checks of a cache (paged_cache.cu).
+tiles_status_t cache_check(const tiles_paged_cache *cache);
+// pos[t] = the position of token t (offsets as for tiles_paged_append), -1 for
+// padding; a position at or beyond max_pos counts as none and is recorded in
+// *status (a plan's word) as kDevBounds.
+cudaError_t positions_launch(const tiles_paged_cache &cache, const int32_t *cu, int n_tokens, int max_pos, int32_t *pos,
+                             uint32_t *status, cudaStream_t st);
+
 // Streaming attention (paged_attn.cu): up to 16 query rows a (row, KV head).
 size_t stream_ws_bytes(int sms, int d);
 cudaError_t stream_launch(const AttnParams &p, int sms, cudaStream_t st);

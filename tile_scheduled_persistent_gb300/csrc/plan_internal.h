@@ -61,6 +61,12 @@ struct ForwardScratch {
     int32_t *tokens = nullptr;    // staging of verify inputs
     unsigned long long *arg_keys = nullptr;  // [T] running argmax keys (zero between passes)
     uint32_t *arg_tickets = nullptr;         // [T] blocks done per token (zero between passes)
+    // passes over a paged cache (tiles_forward_paged)
+    bool paged_ready = false;
+    uint16_t *kv_rows = nullptr;  // new K rows [T][nkv d], then V rows, bf16
+    int32_t *pos = nullptr;       // [T] positions
+    void *paged_ws = nullptr;     // the attention's workspace
+    size_t paged_ws_bytes = 0;
     // tensor maps of the projections' operands: (base, inner, rows, row bytes, box rows) -> map
     std::vector<std::pair<std::array<uint64_t, 5>, tiles::TensorMap>> maps;
 };
