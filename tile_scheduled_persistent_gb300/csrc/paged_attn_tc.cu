@@ -53,7 +53,7 @@ constexpr int kMaskRing = 16;
 constexpr unsigned long long kTimeoutNs = 2000000000ull;
 // The line in which the work is cut counts a pair as its blocks and kPairCost
 // blocks' time for its queries, its output and the change from one to the next.
-constexpr int kPairCost = 3;
+constexpr int kPairCost = 4;
 constexpr float kRise = 8.0f;    // powers of two a maximum may rise before O is rescaled
 
 template <int D, bool I8>
@@ -74,8 +74,13 @@ struct TcShape {
     // tensor memory, 512 columns: scores of the two tiles (128 each), O (D each) and, at D 64,
     // room for the weights of their own; at D 128 they take the place of the scores
     static constexpr bool SPLIT = D == 64;
-    static constexpr int O_COL = 256, P_COL = SPLIT ? 384 : 0, P_TILE = SPLIT ? 64 : 128, P_HALF = HALVES == 1 ? 32 : 64;
+    static constexpr int O_COL = 256, P_COL = SPLIT ? 384 : 0, P_TILE = SPLIT ? 64 : 128,
+                         P_HALF = SPLIT || HALVES == 1 ? 32 : 64;
+    static_assert(O_COL + 2 * D <= (SPLIT ? P_COL : 512) && P_COL + P_TILE + P_HALF + 32 <= 512, "512 columns");
     static constexpr int PART = kPair * (D + 2);        // floats of a partial state: o [D / 4][row][4], m [row], l [row]
+    // bytes: row maxima of the last four blocks and the sums at a pair's end, of a tile's halves;
+    // a kilobyte a softmax warp for the output on its way
+    static constexpr int TOPS = HALVES == 2 ? 5 * 2 * 2 * kTile * 4 : 0, STAGE = SOFTMAX * 1024;
     static constexpr int SCALES = I8 ? 2 * 16 * kBlock * 4 : 0;  // bytes: a block's K and V scales, by block number
 };
 
@@ -98,7 +103,6 @@ struct Ctl {
     int seg_s, seg_h, seg_m;
     long long seg_at, scan[20];
     Seg seg[kSegRing];
-    float top[4][2][2][kTile];   // row maxima of the last four blocks, of a tile's halves (the sums, at a pair's end)
 };
 
 struct SegRec {
@@ -175,6 +179,17 @@ __device__ __forceinline__ void tld64(uint32_t t, uint32_t (&r)[64]) {
         "tcgen05.wait::ld.sync.aligned;"
         : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24), R8(r, 32), R8(r, 40), R8(r, 48), R8(r, 56)
         : "r"(t)
+        : "memory");
+}
+// two times 64, with one wait
+__device__ __forceinline__ void tld128(uint32_t t, uint32_t (&r)[128]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%128];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%129];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24), R8(r, 32), R8(r, 40), R8(r, 48), R8(r, 56), R8(r, 64), R8(r, 72),
+          R8(r, 80), R8(r, 88), R8(r, 96), R8(r, 104), R8(r, 112), R8(r, 120)
+        : "r"(t), "r"(t + 64)
         : "memory");
 }
 __device__ __forceinline__ void tld16(uint32_t t, uint32_t (&r)[16]) {
@@ -324,7 +339,9 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
     extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t *sq = sm;                     // two query tiles
     uint8_t *ring = sm + 2 * S::BLOCK;    // RING blocks
-    Ctl *ctl = reinterpret_cast<Ctl *>(ring + RING * S::BLOCK + S::SCALES);
+    float(*tops)[2][2][kTile] = reinterpret_cast<float(*)[2][2][kTile]>(ring + RING * S::BLOCK + S::SCALES);
+    uint8_t *stages = ring + RING * S::BLOCK + S::SCALES + S::TOPS;
+    Ctl *ctl = reinterpret_cast<Ctl *>(stages + S::STAGE);
     float(*scale)[kMaskRing][kBlock] = reinterpret_cast<float(*)[kMaskRing][kBlock]>(ring + RING * S::BLOCK);  // INT8
     const View &c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
@@ -753,24 +770,24 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             const uint32_t p_tm = tmem + S::P_COL + S::P_TILE * i + S::P_HALF * half + lanes;
             const uint32_t o_tm = tmem + S::O_COL + D * i + DW * half + lanes;
             uint64_t *x_ready = &ctl->x_ready[i][warp & 3];
-            auto top_of = [&](uint32_t block, int h) -> volatile float & { return ctl->top[block & 3][i][h][row]; };
+            auto top_of = [&](uint32_t slot, int h) -> volatile float & { return tops[slot][i][h][row]; };
             uint32_t xs = 0;  // exchanges with the other half so far
-            auto exchange = [&](uint32_t block, float v, float alone) {  // the other half's value
+            auto exchange = [&](uint32_t slot, float v, float alone) {  // the other half's value
                 if (HV == 1) return alone;
-                top_of(block, half) = v;
+                top_of(slot, half) = v;
                 mbar_arrive(x_ready);
                 warp_wait(x_ready, xs);
                 ++xs;
-                return top_of(block, half ^ 1);
+                return top_of(slot, half ^ 1);
             };
-            // unit u of this half of tile row r in shared memory (queries, and the output on its way)
+            // unit u of this half of query row r of the tile in shared memory
             auto staged = [&](int r, int u) {
                 const int x = half * U + u;
                 return reinterpret_cast<uint4 *>(sq + i * S::BLOCK + (x / 8) * S::HALF + r * 128 + (((x % 8) ^ (r & 7)) << 4));
             };
             uint32_t step = 0, kb = 0, n = 0;  // n: ring blocks before the current key block
             uint4 qx[U];
-            bool held = false;  // qx holds the next segment's queries
+            bool held = false;  // the next segment's queries are in shared memory already
             auto load_q = [&](uint32_t k) {
                 const Seg &g = ctl->seg[k % kSegRing];
 #pragma unroll
@@ -781,6 +798,13 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                         qx[v] = __ldg(reinterpret_cast<const uint4 *>(p.q) + g.q_at[i * kTile + r] + (half * U + lane % U));
                 }
             };
+            auto give_q = [&]() {
+#pragma unroll
+                for (int v = 0; v < U; ++v) *staged(32 * (warp & 3) + v * (32 / U) + lane / U, lane % U) = qx[v];
+                fence_proxy_async_smem();
+                mbar_arrive(&ctl->q_ready[i]);
+            };
+            uint8_t *stage = stages + warp * 1024;
             for (uint32_t sg = 0; seg_begin(sg); ++sg) {
                 const Seg &g = ctl->seg[sg % kSegRing];
                 const int r0 = g.m * kPair + i * kTile;  // the tile's first query row
@@ -793,12 +817,11 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     continue;
                 }
                 // queries: U lanes a row, so that a warp reads whole 64- or 128-byte runs
-                if (!held) load_q(sg);
-#pragma unroll
-                for (int v = 0; v < U; ++v) *staged(32 * (warp & 3) + v * (32 / U) + lane / U, lane % U) = qx[v];
+                if (!held) {
+                    load_q(sg);
+                    give_q();
+                }
                 held = false;
-                fence_proxy_async_smem();
-                mbar_arrive(&ctl->q_ready[i]);
                 const int lim = row < rows ? g.len - g.n + group_div(p, r0 + row) : -1;
                 const int all_hi = g.all_hi[i], all_lo = g.all_lo[i];
                 // rows that see nothing need no maximum
@@ -808,12 +831,14 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     ++step;
                     fence_after();
                     // written before the other half's weights of the last block, so visible now
-                    const float other2 = HV == 2 && b - b0 >= 2 ? top_of(kb + 2, half ^ 1) : -INFINITY;
+                    const float other2 = HV == 2 && b - b0 >= 2 ? top_of((kb + 2) & 3, half ^ 1) : -INFINITY;
                     const int t0 = (b < g.nhb ? b : b - g.nhb + g.wb0) * kBlock + CW * half;  // of this thread's positions
                     const uint32_t mask = ctl->mask[kb % kMaskRing] >> (CW / 16 * half);
                     uint32_t x[CW];
-#pragma unroll
-                    for (int j = 0; j < CW; j += 64) tld64(s_tm + j, reinterpret_cast<uint32_t(&)[64]>(x[j]));
+                    if constexpr (CW == 128)
+                        tld128(s_tm, x);
+                    else
+                        tld64(s_tm, x);
                     if constexpr (S::SPLIT) {
                         fence_before();
                         mbar_arrive(&ctl->s_free[i]);
@@ -837,9 +862,12 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                             uint32_t see = low_bits(lim + 1 - tb);
                             if (p.window > 0) see &= ~low_bits(lim - p.window + 1 - tb) | low_bits(p.sinks - tb);
                             see &= ((mask >> (2 * k)) & 1u ? 0xFFFFu : 0u) | ((mask >> (2 * k + 1)) & 1u ? 0xFFFF0000u : 0u);
+                            // most 32s of positions are seen by all of a warp's rows
+                            if (__any_sync(0xFFFFFFFFu, see != 0xFFFFFFFFu)) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (!((see >> j) & 1u)) x[32 * k + j] = 0xFF800000u;
+                                for (int j = 0; j < 32; ++j)
+                                    if (!((see >> j) & 1u)) x[32 * k + j] = 0xFF800000u;
+                            }
                         }
                     }
                     auto block_top = [&]() {
@@ -856,7 +884,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     if (__any_sync(0xFFFFFFFFu, mx == -INFINITY || seen > mx + kRise)) {
                         float nm = seen > mx + kRise ? seen : mx;
                         if (__any_sync(0xFFFFFFFFu, mx == -INFINITY)) {  // rows that have seen nothing yet
-                            const float t = block_top(), u = fmaxf(t, exchange(kb, t, t));
+                            const float t = block_top(), u = fmaxf(t, exchange(kb & 3, t, t));
                             if (!ok) break;
                             if (mx == -INFINITY) nm = u;
                         }
@@ -916,20 +944,22 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                     float l0, l1;
                     unpack2(add2(ls[0], ls[1]), l0, l1);
                     l += l0 + l1;
+                    // (a reference may lag far behind: a weight overflows only beyond 2^127 of it, which
+                    // the output's check for infinities sees; so every fourth block will do)
                     top2 = top1;
-                    top1 = block_top();
-                    if (HV == 2) top_of(kb, half) = top1;
+                    top1 = b - b0 < 2 || (b & 3) == 3 ? block_top() : -INFINITY;
+                    if (HV == 2) top_of(kb & 3, half) = top1;
                 }
                 // ---- the pair's output, or this piece's state
                 if (!ok) break;
                 if (!seg_peek(sg + 1)) break;
-                if (i * kTile < ctl->seg[(sg + 1) % kSegRing].rows && ctl->seg[(sg + 1) % kSegRing].b1 > 0) {
-                    load_q(sg + 1);
-                    held = true;
-                }
+                held = i * kTile < ctl->seg[(sg + 1) % kSegRing].rows && ctl->seg[(sg + 1) % kSegRing].b1 > 0;
+                if (held) load_q(sg + 1);
                 if (!warp_wait(&ctl->o_done[i], step - 1u)) break;
                 fence_after();
-                l += exchange(kb, l, 0.f);
+                // the next pair's queries first: its scores are computed while this output is written
+                if (held) give_q();
+                l += exchange(4, l, 0.f);
                 if (!ok) break;
                 if (b0 == 0 && b1 == g.nb) {
                     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -944,19 +974,23 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                             v[k] = __uint_as_float(o[k]) * inv;
                             sum += fabsf(v[k]);
                         }
-                        *staged(row, d / 8) = make_uint4(cvt_bf2(v[0], v[1]), cvt_bf2(v[2], v[3]), cvt_bf2(v[4], v[5]), cvt_bf2(v[6], v[7]));
-                        *staged(row, d / 8 + 1) =
+                        // through shared memory, so that whole sectors are written
+                        const int flip = (lane >> 2) & 1;
+                        *reinterpret_cast<uint4 *>(stage + lane * 32 + (flip << 4)) =
+                            make_uint4(cvt_bf2(v[0], v[1]), cvt_bf2(v[2], v[3]), cvt_bf2(v[4], v[5]), cvt_bf2(v[6], v[7]));
+                        *reinterpret_cast<uint4 *>(stage + lane * 32 + ((flip ^ 1) << 4)) =
                             make_uint4(cvt_bf2(v[8], v[9]), cvt_bf2(v[10], v[11]), cvt_bf2(v[12], v[13]), cvt_bf2(v[14], v[15]));
+                        __syncwarp();
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int x = 16 * h + (lane >> 1), u = lane & 1, r = 32 * (warp & 3) + x;
+                            if (r < rows)
+                                reinterpret_cast<uint4 *>(p.out)[g.o_at[i * kTile + r] + ((DW * half + d) / 8 + u)] =
+                                    *reinterpret_cast<const uint4 *>(stage + x * 32 + ((u ^ ((x >> 2) & 1)) << 4));
+                        }
+                        __syncwarp();
                     }
                     fence_before();
-                    __syncwarp();
-#pragma unroll
-                    for (int v = 0; v < U; ++v) {
-                        const int r = 32 * (warp & 3) + v * (32 / U) + lane / U;
-                        if (r < rows)
-                            reinterpret_cast<uint4 *>(p.out)[g.o_at[i * kTile + r] + (half * U + lane % U)] = *staged(r, lane % U);
-                    }
-                    __syncwarp();
                     uint32_t again = __ballot_sync(0xFFFFFFFFu, row < rows && !(sum < INFINITY) && g.n > 1);
                     while (again) {
                         const int src = __ffs(again) - 1;
@@ -1094,7 +1128,7 @@ size_t tc_ws_bytes(int sms, int d) { return (size_t)sms * (sizeof(SegRec) + (siz
 template <int D, bool I8>
 static cudaError_t launch(const AttnParams &p, cudaStream_t st) {
     using S = TcShape<D, I8>;
-    constexpr int smem = (2 + S::RING) * S::BLOCK + S::SCALES + (int)sizeof(Ctl);
+    constexpr int smem = (2 + S::RING) * S::BLOCK + S::SCALES + S::TOPS + S::STAGE + (int)sizeof(Ctl);
     static_assert(smem > 116 * 1024 && smem <= kSmemLimit, "one CTA per SM, so that none waits for tensor memory");
     TensorMap mk, mv;
     if constexpr (I8) {
