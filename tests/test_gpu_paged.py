@@ -646,3 +646,119 @@ def test_many_runs_are_bitwise_equal(tsp, d, i8):
             if i % 2:
                 flush.fill_(i)
             assert torch.equal(first, c.run()), i
+
+
+# ------------------------------------------------------------------ windows, pages given back
+@pytest.mark.parametrize("d,i8", [(64, False), (64, True), (128, False), (128, True)])
+@pytest.mark.parametrize("n", [1, 5, 40])
+def test_attention_after_a_trim_needs_no_page_that_is_gone(tsp, d, i8, n):
+    """Pages of 16 in units of up to 128 positions: the windows' first and the sinks'
+    last unit reach into pages that the trim gave back."""
+    import torch
+    for window, sinks in ((20, 4), (33, 0), (100, 17), (49, 16)):
+        lens, ns = [300, 47, 130, 301], [min(n, k) for k in (300, 47, 130, 301)]
+        c = Case(tsp, lens, ns, 4, 2, d, 16, i8, seed=40)
+        # what the tokens of this call see: the trim takes the rows without them
+        c.cache.lens -= torch.tensor(ns, dtype=torch.int32, device="cuda")
+        before = int((c.cache.tables >= 0).sum())
+        c.cache.trim(window, sinks)
+        c.cache.lens += torch.tensor(ns, dtype=torch.int32, device="cuda")
+        assert int((c.cache.tables >= 0).sum()) < before
+        c.check(c.run(window, sinks), window, sinks, weights=2.0 ** -8 if n > 2 else None)
+        c.cache.check()
+
+
+def test_extreme_windows_and_sinks(tsp):
+    big = 2 ** 31 - 1
+    for ns in ([1, 1], [9, 30]):
+        c = Case(tsp, [40, 70], ns, 4, 2, 64, 16, seed=41)
+        whole = c.run()
+        for w, k in ((big, 0), (big, big), (10, big), (80, 3)):
+            assert bool((c.run(w, k) == whole).all()), (w, k)
+        c.check(c.run(1, 0), 1, 0, weights=2.0 ** -8)
+    c.cache.trim(big, 0)
+    c.cache.trim(1, big)
+    assert int((c.cache.tables >= 0).sum()) == 3 + 5
+    c.cache.check()
+
+
+def test_a_captured_prompt_replayed(tsp):
+    """The tensor-core form in a graph, twice in a row and beside an eager call."""
+    import torch
+    c = Case(tsp, [500, 90], [200, 90], 4, 2, 128, 16, seed=42)
+    first = c.run()
+    out = torch.zeros_like(c.q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run(out=out)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        other = c.run()
+        assert torch.equal(out, first) and torch.equal(other, first)
+    c.q.mul_(0.5)
+    g.replay()
+    torch.cuda.synchronize()
+    c.check(out, weights=2.0 ** -8)
+
+
+def test_two_caches_on_two_streams_at_once(tsp):
+    import torch
+    a = Case(tsp, [3000, 2000], [64, 100], 4, 2, 64, 16, seed=43)
+    b = Case(tsp, [5000, 100, 900], [1, 1, 1], 4, 2, 128, 32, seed=44)
+    ra, rb = a.run(), b.run()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        with torch.cuda.stream(sa):
+            oa = a.run()
+        ob = torch.full_like(rb, 7.0)
+        sb.wait_stream(torch.cuda.current_stream())
+        b.run(out=ob, stream=sb)
+        outs.append((oa, ob))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, ra) and torch.equal(y, rb) for x, y in outs)
+
+
+@pytest.mark.parametrize("n_tokens", [1, 2])
+def test_the_smallest_calls(tsp, n_tokens):
+    c = Case(tsp, [n_tokens], [n_tokens], 1, 1, 64, 16, seed=45)
+    c.check(c.run())
+    c = Case(tsp, [n_tokens], [n_tokens], 16, 1, 128, 128, True, seed=46)
+    c.check(c.run(), weights=2.0 ** -8)
+
+
+@pytest.mark.parametrize("page,growth", [(16, 2000), (64, 500)])
+def test_a_resize_of_more_slots_than_threads(tsp, page, growth):
+    """Thousands of pages at once, shared ones among them, against the sequential program."""
+    import torch
+    n = 40
+    cache, m = _cache_and_model(tsp, 40 * (growth // page + 4), n, growth + 200, page, layers=1, hkv=1)
+    for new in ([37] * (n // 2) + [-1] * (n // 2), None, [growth + (s % 7) for s in range(n)], [s * 11 for s in range(n)],
+                [growth] * n):
+        if new is None:
+            src = [-1] * (n // 2) + list(range(n // 2))
+            m.fork(src)
+            m.copies = []
+            cache.fork(torch.tensor(src, dtype=torch.int32, device="cuda"))
+        else:
+            before = _pools(cache)
+            assert m.resize(list(new))
+            cache.resize(torch.tensor(new, dtype=torch.int32, device="cuda"))
+            _moved(before, _pools(cache), m.copies)
+        cache.check()
+        _same(cache, m)
+
+
+def test_more_rows_than_shared_memory_holds(tsp):
+    import torch
+    r = np.random.default_rng(50)
+    n = 2500
+    cache, m = _cache_and_model(tsp, 6000, n, 64, layers=1, hkv=1)
+    for _ in range(3):
+        new = [int(x) for x in r.integers(-1, 30, n)]
+        assert m.resize(new)
+        cache.resize(torch.tensor(new, dtype=torch.int32, device="cuda"))
+        cache.check()
+        _same(cache, m)

@@ -278,9 +278,9 @@ __global__ void __launch_bounds__(kThr, ctas_per_sm(I8)) stream_kernel(const __g
             uint4 kr[NB][2][S::KC], vr[NB][4][S::VC];
             float2 ksc[I8 ? NB : 1][2], vsc[I8 ? NB : 1][2];
             auto unit_t0 = [&](int b) { return (b < it.nhu ? b : b - it.nhu + it.wu0) * UP; };
-            // the pool's group of 16 rows with position tb (a multiple of 16); -1: outside the length, -2: no page
+            // the pool's group of 16 rows with position tb (a multiple of 16); -1: nothing of it is seen, -2: no page
             auto pool_group = [&](int tb) {
-                if (tb >= it.len) return -1;
+                if (tb >= it.len || (tb + 16 <= it.lo && tb >= it.head)) return -1;
                 const int page = __ldg(table + (tb >> c.psl));
                 if (page < 0 || page >= c.n_pages) return -2;
                 return ((page * c.nkv + h) << (c.psl - 4)) + ((tb & (c.ps - 1)) >> 4);

@@ -319,13 +319,18 @@ struct Walk {
     }
 };
 
-__device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity, unsigned long long deadline,
-                                             volatile uint32_t *abort) {
+// False once the wait has taken kTimeoutNs, or another role of the CTA has given up.
+__device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort) {
+    unsigned long long until = 0;
     for (uint32_t spin = 0;; ++spin) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((spin & 63u) == 63u && (*abort || global_timer() > deadline)) {
-            *abort = 1;
-            return false;
+        if ((spin & 63u) == 63u) {
+            const unsigned long long now = global_timer();
+            if (until == 0) until = now + kTimeoutNs;
+            if (*abort || now > until) {
+                *abort = 1;
+                return false;
+            }
         }
     }
 }
@@ -460,14 +465,13 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
     fence_after();
     const uint32_t tmem = ctl->tmem;
     volatile uint32_t *abort = &ctl->abort;
-    const unsigned long long deadline = global_timer() + kTimeoutNs;
     bool ok = true;
     // MMAs and copies this thread has issued, for the way out
     int issued = 0;
 
     if (begin < end) {
         auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = __all_sync(0xFFFFFFFFu, bounded_wait(bar, parity & 1u, deadline, abort));
+            ok = __all_sync(0xFFFFFFFFu, bounded_wait(bar, parity & 1u, abort));
             return ok;
         };
         // the k-th piece of work; false at the end (or after a timeout)
@@ -1038,15 +1042,14 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
     // ---- the way out: after a timeout, what is in flight ends first
     if (!ok) {
         if (lane == 0) atomicOr(reinterpret_cast<uint32_t *>(c.state), kDevTimeout);
-        const unsigned long long d2 = global_timer() + kTimeoutNs;
         uint32_t never = 0;
         if (warp == S::SOFTMAX && issued) {
             commit(&ctl->drain);
-            bounded_wait(&ctl->drain, 0u, d2, &never);
+            bounded_wait(&ctl->drain, 0u, &never);
         }
         if (!I8 && warp == S::LOADER && lane == 0)
             for (int k = max(0, issued - RING); k < issued; ++k)
-                bounded_wait(&ctl->full[k % RING], (uint32_t)(k / RING) & 1u, d2, &never);
+                bounded_wait(&ctl->full[k % RING], (uint32_t)(k / RING) & 1u, &never);
     }
     fence_before();
     __syncthreads();

@@ -815,8 +815,10 @@ tiles_status_t tiles_paged_attention(const tiles_paged_cache *cache, int32_t lay
     p.G = n_q_heads / d.n_kv_heads;
     p.g_mul = (unsigned)(((1ull << 32) + (unsigned)p.G - 1) / (unsigned)p.G);
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
-    p.window = window;
-    p.sinks = window > 0 ? sinks : 0;
+    // a window as long as the longest row hides nothing
+    const int cap = d.table_width * d.page_size;
+    p.window = window >= cap ? 0 : window;
+    p.sinks = p.window > 0 ? std::min(sinks, cap) : 0;
     p.ws = static_cast<float *>(workspace);
     p.ctas = 0;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
