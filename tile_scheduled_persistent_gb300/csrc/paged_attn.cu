@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(kThr, ctas_per_sm(I8)) stream_kernel(const __g
     const int cta = blockIdx.x;
     JoinRec *recs = reinterpret_cast<JoinRec *>(p.ws);
     float *parts = p.ws + (size_t)p.ctas * (sizeof(JoinRec) / 4);
+    after_previous();
     if (tid == 0) recs[cta].parts = 0;
 
     // ---- where this CTA's piece of the line begins
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(kThr) join_kernel(const __grid_constant__ Attn
     __shared__ float2 sl[GR];
     __shared__ int bad_row;
     const int tid = threadIdx.x, cta = blockIdx.x, r = blockIdx.y;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     const JoinRec rec = reinterpret_cast<const JoinRec *>(p.ws)[cta];
     if (rec.parts == 0) return;
     bool bad = false;
@@ -734,20 +735,9 @@ size_t stream_ws_bytes(int sms, int d) {
 
 template <int D, bool I8, int RT>
 static cudaError_t launch(const AttnParams &p, cudaStream_t st) {
-    stream_kernel<D, I8, RT><<<p.ctas, kThr, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_next(stream_kernel<D, I8, RT>, dim3((unsigned)p.ctas), dim3(kThr), 0, st, p);
     if (e != cudaSuccess) return e;
-    // the join's blocks may be set up while the last pieces are still at work
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)RT);
-    cfg.blockDim = dim3(kThr);
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, I8, RT>, p);
+    return launch_next(join_kernel<D, I8, RT>, dim3((unsigned)p.ctas, (unsigned)RT), dim3(kThr), 0, st, p);
 }
 
 cudaError_t stream_launch(const AttnParams &p0, int sms, cudaStream_t st) {

@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
     SegRec *recs = reinterpret_cast<SegRec *>(p.ws);
     float *parts = p.ws + (size_t)p.ctas * (sizeof(SegRec) / 4);
+    after_previous();
     if (smem_u32(sm) & 1023u) {  // the swizzle counts on it
         if (tid == 0) {
             recs[cta].parts = 0;
@@ -1069,7 +1070,7 @@ __global__ void __launch_bounds__(256) tc_join_kernel(const __grid_constant__ At
     __shared__ __align__(16) uint16_t so[32][D + 8];
     __shared__ int again[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x, q0 = blockIdx.y * 32;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     const SegRec rec = reinterpret_cast<const SegRec *>(p.ws)[cta];
     if (rec.parts == 0) return;
     bool bad = false;
@@ -1145,18 +1146,8 @@ static cudaError_t launch(const AttnParams &p, cudaStream_t st) {
     }
     cudaError_t e = cudaFuncSetAttribute(tc_kernel<D, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    tc_kernel<D, I8><<<p.ctas, S::THREADS, smem, st>>>(p, mk, mv);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)p.ctas, kPair / 32);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tc_join_kernel<D, I8>, p);
+    if ((e = launch_next(tc_kernel<D, I8>, dim3((unsigned)p.ctas), dim3(S::THREADS), smem, st, p, mk, mv)) != cudaSuccess) return e;
+    return launch_next(tc_join_kernel<D, I8>, dim3((unsigned)p.ctas, kPair / 32), dim3(256), 0, st, p);
 }
 
 cudaError_t tc_launch(const AttnParams &p0, int sms, cudaStream_t st) {

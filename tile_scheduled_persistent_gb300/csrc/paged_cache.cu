@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kBookThreads) resize_kernel(View c, const int3
     const Book b = book_of(c.state, c.n_pages, c.n_seqs);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool shared = c.n_seqs <= kRowsShared;
+    after_previous();
     const int P = c.n_pages, W = c.width, ps = c.ps;
     uint32_t flags = 0;
     if (tid == 0) n_copies = 0;
@@ -311,7 +312,7 @@ __device__ __forceinline__ void move_bytes(const uint8_t *src, uint8_t *dst, lon
 
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(View c, int remap) {
     const Book b = book_of(c.state, c.n_pages, c.n_seqs);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     const int n = *b.copies;
     const long long block = (long long)c.nkv * c.ps * c.d * (c.i8 ? 1 : 2), scales = (long long)c.nkv * c.ps * 4;
     // one work item: a page of one layer of K or of V
@@ -349,6 +350,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(View c, int remap) {
 __global__ void __launch_bounds__(32) fork_kernel(View c, const int32_t *__restrict__ src_rows) {
     const Book b = book_of(c.state, c.n_pages, c.n_seqs);
     const int s = blockIdx.x, lane = threadIdx.x, W = c.width;
+    after_previous();
     const int from = src_rows[s];
     if (from < 0) return;
     bool ok = from < c.n_seqs && from != s && src_rows[from] < 0 && c.lens[s] == 0;
@@ -386,6 +388,7 @@ __global__ void __launch_bounds__(32) fork_kernel(View c, const int32_t *__restr
 __global__ void __launch_bounds__(32) trim_kernel(View c, int window, int sinks) {
     const Book b = book_of(c.state, c.n_pages, c.n_seqs);
     const int s = blockIdx.x, lane = threadIdx.x, ps = c.ps;
+    after_previous();
     int len = c.lens[s];
     if (len > c.width * ps) len = c.width * ps;
     const int last = len - window;  // positions <= last are seen by no later token
@@ -409,6 +412,7 @@ __global__ void __launch_bounds__(kBookThreads) compact_kernel(View c) {
     __shared__ int warps[32];
     const Book b = book_of(c.state, c.n_pages, c.n_seqs);
     const int tid = threadIdx.x, P = c.n_pages;
+    after_previous();
     int live = 0, sum;
     for (int p = tid; p < P; p += kBookThreads) live += b.refs[p] > 0;
     block_excl(live, warps, &sum);
@@ -437,11 +441,13 @@ __global__ void __launch_bounds__(kBookThreads) compact_kernel(View c) {
 }
 
 // ------------------------------------------------------------------ append
-// One warp per (token, KV head); lanes take 8 elements each, so a row is D / 8
-// lanes and a warp writes 256 / D rows: K and V rows of its heads. INT8 rows
-// are quantized by the lanes that hold them (s = max |x| / 127 over the row, a
-// butterfly over D / 8 lanes).
-constexpr int kAppendWarps = 8;
+// One warp per token and group of its rows; lanes take 8 elements each, so a row
+// is D / 8 lanes and a warp holds 256 / D rows (K and V rows of the token's heads) a
+// step. Bound by the chain from a token's number to its row's place (offsets, length,
+// page), so the rows are read before it, four steps at once. INT8 rows are quantized
+// by the lanes that hold them (s = max |x| / 127 over the row, a butterfly over D / 8
+// lanes).
+constexpr int kAppendWarps = 8, kAppendSteps = 4;
 
 // The row of token t: the last s with cu[s] <= t, or -1 for padding.
 __device__ __forceinline__ int row_of_token(const int32_t *__restrict__ cu, int n_seqs, int t, int lane) {
@@ -467,7 +473,23 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
     constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes a row, rows a warp and step
     const int lane = threadIdx.x & 31, sub = lane / LPR, e = (lane % LPR) * 8;
     const int t = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    after_previous();
     if (t >= n_tokens) return;
+    const int rows = 2 * c.nkv;  // (K or V, head)
+    const int r_first = blockIdx.y * kAppendSteps * RPW, r_step = gridDim.y * kAppendSteps * RPW;
+    uint4 xs[kAppendSteps];
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < kAppendSteps; ++i) {
+            const int r = r0 + i * RPW + sub;
+            const bool isv = r >= c.nkv;
+            const int h = isv ? r - c.nkv : r;
+            xs[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows)
+                xs[i] = __ldg(reinterpret_cast<const uint4 *>(isv ? v + t * v_t + h * v_h + e : k + t * k_t + h * k_h + e));
+        }
+    };
+    load(r_first);
     int s, pos;
     if (cu) {
         s = row_of_token(cu, c.n_seqs, t, lane);
@@ -479,44 +501,45 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
     }
     if (pos < 0) return;
     int page = -1;
-    if (pos < c.width * c.ps) page = __ldg(c.tables + (size_t)s * c.width + pos / c.ps);
+    if (pos < c.width * c.ps) page = __ldg(c.tables + (size_t)s * c.width + (pos >> c.psl));
     if (page < 0 || page >= c.n_pages) {
         if (lane == 0) atomicOr(reinterpret_cast<uint32_t *>(c.state), kDevBounds);
         return;
     }
-    const int rows = 2 * c.nkv;  // (K or V, head)
-    for (int r0 = blockIdx.y * RPW; r0 < rows; r0 += gridDim.y * RPW) {
-        const int r = r0 + sub;
-        const bool in = r < rows, isv = r >= c.nkv;
-        const int h = isv ? r - c.nkv : r;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (in)
-            x = __ldg(reinterpret_cast<const uint4 *>(isv ? v + t * v_t + h * v_h + e : k + t * k_t + h * k_h + e));
-        const size_t at = ((size_t)page * c.nkv + h) * c.ps + pos % c.ps;  // row of the layer's pool
-        if constexpr (!I8) {
-            if (in) *reinterpret_cast<uint4 *>((isv ? c.v : c.k) + (at * D + e) * 2) = x;
-        } else {
-            float f[8], amax = 0.f;
-            unpack8(x, f);
-            if (in && !isv && c.k_shift) {
+    for (int r0 = r_first; r0 < rows; r0 += r_step) {
+        if (r0 != r_first) load(r0);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = __fsub_rn(f[i], __ldg(c.k_shift + h * D + e + i));
-            }
+        for (int i0 = 0; i0 < kAppendSteps; ++i0) {
+            const int r = r0 + i0 * RPW + sub;
+            const bool in = r < rows, isv = r >= c.nkv;
+            const int h = isv ? r - c.nkv : r;
+            const uint4 x = xs[i0];
+            const size_t at = ((size_t)page * c.nkv + h) * c.ps + (pos & (c.ps - 1));  // row of the layer's pool
+            if constexpr (!I8) {
+                if (in) *reinterpret_cast<uint4 *>((isv ? c.v : c.k) + (at * D + e) * 2) = x;
+            } else {
+                float f[8], amax = 0.f;
+                unpack8(x, f);
+                if (in && !isv && c.k_shift) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+                    for (int i = 0; i < 8; ++i) f[i] = __fsub_rn(f[i], __ldg(c.k_shift + h * D + e + i));
+                }
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-            const float sc = __fdiv_rn(amax, 127.0f);
-            uint32_t w[2] = {0u, 0u};
+                for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float qf = sc > 0.f ? rintf(__fdiv_rn(f[i], sc)) : 0.f;
-                const int q = (int)fminf(fmaxf(qf, -127.f), 127.f);
-                w[i / 4] |= ((uint32_t)q & 0xFFu) << (8 * (i % 4));
-            }
-            if (in) {
-                *reinterpret_cast<uint2 *>((isv ? c.v : c.k) + at * D + e) = make_uint2(w[0], w[1]);
-                if (e == 0) (isv ? c.vs : c.ks)[at] = sc;
+                for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+                const float sc = __fdiv_rn(amax, 127.0f);
+                uint32_t w[2] = {0u, 0u};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float qf = sc > 0.f ? rintf(__fdiv_rn(f[i], sc)) : 0.f;
+                    const int q = (int)fminf(fmaxf(qf, -127.f), 127.f);
+                    w[i / 4] |= ((uint32_t)q & 0xFFu) << (8 * (i % 4));
+                }
+                if (in) {
+                    *reinterpret_cast<uint2 *>((isv ? c.v : c.k) + at * D + e) = make_uint2(w[0], w[1]);
+                    if (e == 0) (isv ? c.vs : c.ks)[at] = sc;
+                }
             }
         }
     }
@@ -527,6 +550,7 @@ __global__ void __launch_bounds__(32) positions_kernel(const int32_t *__restrict
                                                        const int32_t *__restrict__ cu, int max_pos, int32_t *pos,
                                                        uint32_t *status) {
     const int t = blockIdx.x, lane = threadIdx.x;
+    after_previous();
     int p = -1;
     if (cu) {
         const int s = row_of_token(cu, n_seqs, t, lane);
@@ -544,8 +568,8 @@ __global__ void __launch_bounds__(32) positions_kernel(const int32_t *__restrict
 
 cudaError_t positions_launch(const tiles_paged_cache &cache, const int32_t *cu, int n_tokens, int max_pos, int32_t *pos,
                              uint32_t *status, cudaStream_t st) {
-    positions_kernel<<<n_tokens, 32, 0, st>>>(cache.lens, cache.desc.n_seqs, cu, max_pos, pos, status);
-    return cudaGetLastError();
+    return launch_next(positions_kernel, dim3((unsigned)n_tokens), dim3(32), 0, st, cache.lens, cache.desc.n_seqs, cu, max_pos, pos,
+                       status);
 }
 
 }  // namespace paged
@@ -645,21 +669,7 @@ int64_t attn_ws_bytes(const tiles_paged_desc &d, int n_q_heads, int max_tokens, 
                                                                   : tc_ws_bytes(sms, d.head_dim));
 }
 
-// The kernel that moves the pages, set up while the one that lists them runs.
-tiles_status_t launch_move(const View &v, int remap, int sms, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)(sms * 8));
-    cfg.blockDim = dim3(kMoveThreads);
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, move_kernel, v, remap) == cudaSuccess ? TILES_OK : TILES_ERR_CUDA;
-}
-
-tiles_status_t launched() { return cudaGetLastError() == cudaSuccess ? TILES_OK : TILES_ERR_CUDA; }
+tiles_status_t launched(cudaError_t e) { return e == cudaSuccess ? TILES_OK : TILES_ERR_CUDA; }
 
 }  // namespace
 
@@ -694,25 +704,24 @@ tiles_status_t tiles_paged_resize(const tiles_paged_cache *cache, const int32_t 
     if ((st = sm_count(&sms)) != TILES_OK) return st;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const View v = view_of(*cache, 0);
-    resize_kernel<<<1, kBookThreads, 0, cs>>>(v, new_lens);
-    if ((st = launched()) != TILES_OK) return st;
-    return launch_move(v, 0, sms, cs);
+    if ((st = launched(launch_next(resize_kernel, dim3(1), dim3(kBookThreads), 0, cs, v, new_lens))) != TILES_OK) return st;
+    return launched(launch_next(move_kernel, dim3((unsigned)(sms * 8)), dim3(kMoveThreads), 0, cs, v, 0));
 }
 
 tiles_status_t tiles_paged_fork(const tiles_paged_cache *cache, const int32_t *src_rows, void *stream) {
     const tiles_status_t st = check_cache(cache);
     if (st != TILES_OK) return st;
     if (!src_rows || !al4(src_rows)) return TILES_ERR_INVALID_ARG;
-    fork_kernel<<<cache->desc.n_seqs, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(view_of(*cache, 0), src_rows);
-    return launched();
+    return launched(launch_next(fork_kernel, dim3((unsigned)cache->desc.n_seqs), dim3(32), 0,
+                                reinterpret_cast<cudaStream_t>(stream), view_of(*cache, 0), src_rows));
 }
 
 tiles_status_t tiles_paged_trim(const tiles_paged_cache *cache, int32_t window, int32_t sinks, void *stream) {
     const tiles_status_t st = check_cache(cache);
     if (st != TILES_OK) return st;
     if (window < 1 || sinks < 0) return TILES_ERR_INVALID_ARG;
-    trim_kernel<<<cache->desc.n_seqs, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(view_of(*cache, 0), window, sinks);
-    return launched();
+    return launched(launch_next(trim_kernel, dim3((unsigned)cache->desc.n_seqs), dim3(32), 0,
+                                reinterpret_cast<cudaStream_t>(stream), view_of(*cache, 0), window, sinks));
 }
 
 tiles_status_t tiles_paged_compact(const tiles_paged_cache *cache, void *stream) {
@@ -722,9 +731,8 @@ tiles_status_t tiles_paged_compact(const tiles_paged_cache *cache, void *stream)
     if ((st = sm_count(&sms)) != TILES_OK) return st;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const View v = view_of(*cache, 0);
-    compact_kernel<<<1, kBookThreads, 0, cs>>>(v);
-    if ((st = launched()) != TILES_OK) return st;
-    return launch_move(v, 1, sms, cs);
+    if ((st = launched(launch_next(compact_kernel, dim3(1), dim3(kBookThreads), 0, cs, v))) != TILES_OK) return st;
+    return launched(launch_next(move_kernel, dim3((unsigned)(sms * 8)), dim3(kMoveThreads), 0, cs, v, 1));
 }
 
 tiles_status_t tiles_paged_append(const tiles_paged_cache *cache, int32_t layer, const void *k, int64_t k_stride_token,
@@ -741,23 +749,18 @@ tiles_status_t tiles_paged_append(const tiles_paged_cache *cache, int32_t layer,
         return TILES_ERR_INVALID_ARG;
     const View c = view_of(*cache, layer);
     const uint16_t *kp = static_cast<const uint16_t *>(k), *vp = static_cast<const uint16_t *>(v);
-    // few tokens: a warp per group of rows of a token; many: a warp takes all of a token's rows
+    // a warp's steps a token: all at once, so that a token's rows go to as few warps as that takes
     const int steps = (2 * d.n_kv_heads * d.head_dim / 8 + 31) / 32;
-    const int gy = n_tokens >= 2048 ? 1 : std::min(steps, 65535);
+    const int gy = std::min((steps + kAppendSteps - 1) / kAppendSteps, 65535);
     const dim3 grid((unsigned)((n_tokens + kAppendWarps - 1) / kAppendWarps), (unsigned)gy);
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-#define TILES_APPEND(D, I8)                                                                                    \
-    append_kernel<D, I8><<<grid, kAppendWarps * 32, 0, cs>>>(c, kp, k_stride_token, k_stride_head, vp, v_stride_token, \
-                                                             v_stride_head, cu_tokens, n_tokens)
-    if (d.head_dim == 64) {
-        if (c.i8) TILES_APPEND(64, true);
-        else TILES_APPEND(64, false);
-    } else {
-        if (c.i8) TILES_APPEND(128, true);
-        else TILES_APPEND(128, false);
-    }
-#undef TILES_APPEND
-    return launched();
+    auto go = [&](auto kernel) {
+        return launched(launch_next(kernel, grid, dim3(kAppendWarps * 32), 0, cs, c, kp, (long long)k_stride_token,
+                                    (long long)k_stride_head, vp, (long long)v_stride_token, (long long)v_stride_head, cu_tokens,
+                                    n_tokens));
+    };
+    if (d.head_dim == 64) return c.i8 ? go(append_kernel<64, true>) : go(append_kernel<64, false>);
+    return c.i8 ? go(append_kernel<128, true>) : go(append_kernel<128, false>);
 }
 
 tiles_status_t tiles_paged_workspace_bytes(const tiles_paged_desc *desc, int32_t n_q_heads, int32_t max_tokens,
