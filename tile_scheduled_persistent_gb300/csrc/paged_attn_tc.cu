@@ -319,18 +319,14 @@ struct Walk {
     }
 };
 
-// False once the wait has taken kTimeoutNs, or another role of the CTA has given up.
-__device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort) {
-    unsigned long long until = 0;
+// False past the deadline, or once another role of the CTA has given up.
+__device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity, unsigned long long deadline,
+                                             volatile uint32_t *abort) {
     for (uint32_t spin = 0;; ++spin) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((spin & 63u) == 63u) {
-            const unsigned long long now = global_timer();
-            if (until == 0) until = now + kTimeoutNs;
-            if (*abort || now > until) {
-                *abort = 1;
-                return false;
-            }
+        if ((spin & 63u) == 63u && (*abort || global_timer() > deadline)) {
+            *abort = 1;
+            return false;
         }
     }
 }
@@ -466,17 +462,22 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
     fence_after();
     const uint32_t tmem = ctl->tmem;
     volatile uint32_t *abort = &ctl->abort;
+    // set anew for each piece of work, so that it bounds a wait and not the kernel
+    unsigned long long deadline = global_timer() + kTimeoutNs;
     bool ok = true;
     // MMAs and copies this thread has issued, for the way out
     int issued = 0;
 
     if (begin < end) {
         auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = __all_sync(0xFFFFFFFFu, bounded_wait(bar, parity & 1u, abort));
+            ok = __all_sync(0xFFFFFFFFu, bounded_wait(bar, parity & 1u, deadline, abort));
             return ok;
         };
         // the k-th piece of work; false at the end (or after a timeout)
-        auto seg_begin = [&](uint32_t k) { return warp_wait(&ctl->seg_full[k % kSegRing], k / kSegRing) && ctl->seg[k % kSegRing].b1 > 0; };
+        auto seg_begin = [&](uint32_t k) {
+            deadline = global_timer() + kTimeoutNs;
+            return warp_wait(&ctl->seg_full[k % kSegRing], k / kSegRing) && ctl->seg[k % kSegRing].b1 > 0;
+        };
         auto seg_peek = [&](uint32_t k) { return warp_wait(&ctl->seg_full[k % kSegRing], k / kSegRing); };
         auto seg_end = [&](uint32_t k) {
             __syncwarp();
@@ -490,7 +491,10 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             w.m = ctl->seg_m;
             w.load(p);
             uint32_t k = 0;
-            auto slot_free = [&]() { return k < kSegRing || warp_wait(&ctl->seg_empty[k % kSegRing], k / kSegRing - 1u); };
+            auto slot_free = [&]() {
+                deadline = global_timer() + kTimeoutNs;
+                return k < kSegRing || warp_wait(&ctl->seg_empty[k % kSegRing], k / kSegRing - 1u);
+            };
             // in cost units: where the work begins in its first pair, how much there is. Of a pair
             // that begins at unit 0, units kPairCost + b are block b.
             int at = (int)(begin - ctl->seg_at), left = (int)(end - begin);
@@ -1044,13 +1048,14 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
     if (!ok) {
         if (lane == 0) atomicOr(reinterpret_cast<uint32_t *>(c.state), kDevTimeout);
         uint32_t never = 0;
+        deadline = global_timer() + kTimeoutNs;
         if (warp == S::SOFTMAX && issued) {
             commit(&ctl->drain);
-            bounded_wait(&ctl->drain, 0u, &never);
+            bounded_wait(&ctl->drain, 0u, deadline, &never);
         }
         if (!I8 && warp == S::LOADER && lane == 0)
             for (int k = max(0, issued - RING); k < issued; ++k)
-                bounded_wait(&ctl->full[k % RING], (uint32_t)(k / RING) & 1u, &never);
+                bounded_wait(&ctl->full[k % RING], (uint32_t)(k / RING) & 1u, deadline, &never);
     }
     fence_before();
     __syncthreads();
