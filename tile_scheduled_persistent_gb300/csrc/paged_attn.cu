@@ -40,9 +40,9 @@ namespace paged {
 
 constexpr int kWarps = 4;
 constexpr int kThr = kWarps * 32;
-// CTAs an SM: what 168 registers a thread allow, 128 for an INT8 cache (half the bytes in
-// flight a warp, but more warps to widen codes while others wait)
-constexpr int ctas_per_sm(bool i8) { return i8 ? 4 : 3; }
+// What 168 registers a thread allow. (An INT8 cache with 4 CTAs of 128 registers, which
+// spill: 82 us in place of 77 for 64 rows of up to 32,768 under a window of 4,096.)
+constexpr int kCtasPerSm = 3;
 // The line counts an item as its units and kItemCost for its queries, its first loads and
 // its merge (about 4 us, in which a CTA takes 8 units); a piece is at least kMinCost.
 constexpr int kItemCost = 8, kMinCost = kWarps;
@@ -130,7 +130,7 @@ struct Shape {
 };
 
 template <int D, bool I8, int RT>
-__global__ void __launch_bounds__(kThr, ctas_per_sm(I8)) stream_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kThr, kCtasPerSm) stream_kernel(const __grid_constant__ AttnParams p) {
     using S = Shape<D, I8, RT>;
     constexpr int NB = S::NB, UP = S::UP, RH = S::RH, LD = S::LD;
     __shared__ long long wsum[kWarps];
@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(kThr) join_kernel(const __grid_constant__ Attn
 
 // ------------------------------------------------------------------ host side
 size_t stream_ws_bytes(int sms, int d) {
-    return (size_t)sms * ctas_per_sm(true) * (sizeof(JoinRec) + (size_t)2 * 16 * (d + 4) * 4);
+    return (size_t)sms * kCtasPerSm * (sizeof(JoinRec) + (size_t)2 * 16 * (d + 4) * 4);
 }
 
 template <int D, bool I8, int RT>
@@ -742,7 +742,7 @@ static cudaError_t launch(const AttnParams &p, cudaStream_t st) {
 
 cudaError_t stream_launch(const AttnParams &p0, int sms, cudaStream_t st) {
     AttnParams p = p0;
-    p.ctas = sms * ctas_per_sm(p.c.i8);
+    p.ctas = sms * kCtasPerSm;
     const bool small = p.max_tokens * p.G <= 8;
     if (p.c.d == 64) {
         if (p.c.i8) return small ? launch<64, true, 8>(p, st) : launch<64, true, 16>(p, st);
