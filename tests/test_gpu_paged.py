@@ -112,15 +112,16 @@ class Case:
                              sinks=sinks, **kw)
         return out
 
-    def check(self, out, window=0, sinks=0, weights=None, scale=None):
-        """weights: what a weight may be off by, before the scores' error."""
+    def check(self, out, window=0, sinks=0, weights=None, scale=None, least=0.0):
+        """weights: what a weight may be off by, before the scores' error; least: what an
+        output may be off by where all of a dimension's weight lies on tiny weights."""
         if weights is None:
             weights = 2.0 ** -11 if self.int8 else 2.0 ** -16
         n = int(self.cu[-1])
         ref, spread, serr = R.attention(self.q[:n].double().cpu().numpy(), self.keys, self.values, self.lens, self.cu,
                                         self.d ** -0.5 if scale is None else scale, window, sinks)
         got = out.double().cpu().numpy()
-        tol = R.BF16_HALF * np.abs(ref) + (weights + 2.0 ** -20 + serr) * spread + 1e-30
+        tol = R.BF16_HALF * np.abs(ref) + (weights + 2.0 ** -20 + serr) * spread + 1e-30 + least
         err = np.abs(got[:n] - ref)
         assert np.isfinite(got[:n]).all()
         assert (err <= tol).all(), (float((err / tol).max()), np.argwhere(err > tol)[:5])
@@ -203,8 +204,9 @@ def test_large_scores_and_far_apart_values(tsp, i8):
     """Scores of several hundred: the running maximum does its work."""
     c = Case(tsp, [300, 77], [1, 1], 4, 2, 64, 16, i8, seed=8, amp=60.0)
     c.check(c.run(cu=False))
-    c = Case(tsp, [300, 77], [40, 30], 4, 2, 64, 16, i8, seed=8, amp=60.0)
-    c.check(c.run(), weights=2.0 ** -8)
+    for d in (64, 128):
+        c = Case(tsp, [300, 77], [40, 30], 4, 2, d, 16, i8, seed=8, amp=60.0)
+        c.check(c.run(), weights=2.0 ** -8)
 
 
 @pytest.mark.parametrize("ns", [3, 30])
@@ -762,3 +764,73 @@ def test_more_rows_than_shared_memory_holds(tsp):
         cache.resize(torch.tensor(new, dtype=torch.int32, device="cuda"))
         cache.check()
         _same(cache, m)
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_that_climb_by_hundreds(tsp, d, i8):
+    """Keys that grow along the sequence, so that each block's scores lie far above the
+    last one's (beyond what FP32 holds relative to the first): prompts, single tokens in a
+    call with prompts, and single tokens alone; and keys that all but one of shrink."""
+    import torch
+    for seed, factor in ((60, lambda t, n: 1.0 + 120.0 * t / n), (61, lambda t, n: 120.0 * (t == n // 3) + 0.01)):
+        lens, ns = [700, 513, 90], [30, 1, 90]
+        c = Case(tsp, lens, ns, 4, 2, d, 16, i8, seed=seed)
+        (kp, ks), _ = c.cache.key_pool(), c.cache.value_pool()
+        for s, n in enumerate(lens):
+            for t in range(n):
+                f = factor(t, n)
+                at = (0, int(c.tables[s, t // 16]), slice(None), t % 16)
+                if i8:
+                    new = (ks[at].double() * f).float()
+                    ks[at] = new
+                    c.keys[s][t] = kp[at].double().cpu().numpy() * new.double().cpu().numpy()[:, None]
+                else:
+                    kp[at] = (kp[at].float() * f).to(torch.bfloat16)
+                    c.keys[s][t] = kp[at].double().cpu().numpy()
+        c.check(c.run(), weights=2.0 ** -8)
+        c.check(c.run(300, 3), 300, 3, weights=2.0 ** -8)
+        c.cache.check()
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_that_rise_by_any_power_of_two(tsp, d, i8):
+    """One position far above all before it, by up to beyond what FP32's exponent holds, whose
+    value is zero in the first half of the dimensions: there a later position 2^-20 of it
+    shows. Short rows, which several blocks may share, and enough of them that most do not."""
+    import torch
+    rises = [0.0, 60.0, 100.0, 125.0, 126.0, 126.5, 127.0, 127.5, 128.0, 150.0, 252.0, 254.0, 500.0]
+    for copies, cols in ((1, (0, 130, 300, 511)), (4, (130, 300))):
+        lens, peaks = [], []
+        for x in rises:
+            for col in cols:
+                lens += [640] * copies
+                peaks += [(x, col)] * copies
+        c = Case(tsp, lens, [2] * len(lens), 4, 4, d, 64, i8, seed=62)
+        (kp, ks), (vp, vs) = c.cache.key_pool(), c.cache.value_pool()
+        c.q.zero_()
+        c.q[:, :, 0] = 1.0
+        for s, (x, col) in enumerate(peaks):
+            k0 = np.zeros(640)
+            k0[col], k0[col + 100] = x, x - 20.0
+            for t in range(640):
+                c.keys[s][t, :, 0] = k0[t]
+            c.values[s][col, :, : d // 2] = 0.0
+            pages = torch.from_numpy(c.tables[s][:10]).cuda().long()
+            at = torch.from_numpy(k0).cuda().view(10, 1, 64)
+            if i8:
+                kp[0, pages, :, :, 0] = torch.where(at == 0, 0, 127).to(torch.int8).expand(10, 4, 64)
+                ks[0, pages] = (at / 127).float().expand(10, 4, 64)
+                c.keys[s][:, :, 0] = (k0 / 127).astype(np.float32).astype(np.float64)[:, None] * 127
+            else:
+                kp[0, pages, :, :, 0] = at.to(torch.bfloat16).expand(10, 4, 64)
+            vp[0, int(pages[col // 64]), :, col % 64, : d // 2] = 0
+        # The single tokens' kernel holds a weight times its value's scale as an FP16 number of
+        # steps of 2^-24, where the largest weight times a power of two below twice the largest
+        # scale is 2^12: off by half a step, 2^-37 of those. Over 640 codes of 127 at most, and
+        # scales of max |v| / 127: 640 * 2^-36 * max |v|, with a sum of weights of 1 or more.
+        least = 640 * 2.0 ** -36 * max(np.abs(v).max() for v in c.values) if i8 else 0.0
+        c.check(c.run(scale=float(np.log(2.0)), max_tokens=2), weights=2.0 ** -8, scale=np.log(2.0), least=least)
+        c.check(c.run(scale=float(np.log(2.0)), max_tokens=20), weights=2.0 ** -8, scale=np.log(2.0))
+        c.cache.check()
