@@ -834,3 +834,29 @@ def test_scores_that_rise_by_any_power_of_two(tsp, d, i8):
         c.check(c.run(scale=float(np.log(2.0)), max_tokens=2), weights=2.0 ** -8, scale=np.log(2.0), least=least)
         c.check(c.run(scale=float(np.log(2.0)), max_tokens=20), weights=2.0 ** -8, scale=np.log(2.0))
         c.cache.check()
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_tile_of_rows_beside_an_infinity_in_a_long_cache(tsp, d, i8):
+    """An infinite value that only the last token sees: the other 254 rows of its tiles are
+    computed again over 32,768 positions, well within the limit of the waits."""
+    import torch
+    c = Case(tsp, [32768], [128], 2, 1, d, 64, i8, seed=63)
+    (vp, vs) = c.cache.value_pool()
+    at = (0, int(c.tables[0, 511]), 0, 63)
+    if i8:
+        vs[at] = float("inf")
+        vp[at] = 127
+    else:
+        vp[at] = float("inf")
+    out = c.run()
+    c.cache.check()
+    assert not torch.isfinite(out[127].float()).any()
+    got = out.double().cpu().numpy()
+    assert np.isfinite(got[:127]).all()
+    for tok in (0, 60, 126):                                # at position 32,640 + tok
+        ref, spread, serr = R.attention(c.q.double().cpu().numpy()[tok: tok + 1], [c.keys[0][:32641 + tok]],
+                                        [c.values[0][:32641 + tok]], [32641 + tok], np.array([0, 1]), d ** -0.5)
+        tol = R.BF16_HALF * np.abs(ref) + (2.0 ** -8 + 2.0 ** -20 + serr) * spread + 1e-30
+        assert (np.abs(got[tok] - ref[0]) <= tol[0]).all(), tok

@@ -107,7 +107,7 @@ constexpr int kSegRing = 3;
 struct Ctl {
     uint64_t full[kMaxRing], empty[kMaxRing], fix, drain, q_ready[2], s_full[2], s_free[2], p_full[2], o_done[2], x_ready[2][4];
     uint64_t seg_full[kSegRing], seg_empty[kSegRing];
-    uint32_t tmem, abort;
+    uint32_t tmem, abort, again;     // again: some row of the output came out infinite or NaN
     uint32_t mask[kMaskRing];    // pages of a key block that are there, by block number
     int seg_s, seg_h, seg_m;
     long long seg_at, scan[20];
@@ -276,9 +276,9 @@ __device__ __forceinline__ int pairs_of(const AttnParams &p, const RowSpan &r) {
 
 // Cost of one head of each of 32 rows (one a lane): rows of several pairs are
 // added up by the whole warp.
-__device__ __forceinline__ int row_cost(const AttnParams &p, const RowSpan &r, int lane) {
+__device__ __forceinline__ long long row_cost(const AttnParams &p, const RowSpan &r, int lane) {
     const int np = pairs_of(p, r);
-    int nb = np == 1 ? pair_span(p, r, 0).cost() : 0;
+    long long nb = np == 1 ? pair_span(p, r, 0).cost() : 0;
     uint32_t many = __ballot_sync(0xFFFFFFFFu, np > 1);
     while (many) {
         const int src = __ffs(many) - 1;
@@ -288,7 +288,7 @@ __device__ __forceinline__ int row_cost(const AttnParams &p, const RowSpan &r, i
         q.n = __shfl_sync(0xFFFFFFFFu, r.n, src);
         q.len = __shfl_sync(0xFFFFFFFFu, r.len, src);
         const int k = pairs_of(p, q);
-        int sum = 0;
+        long long sum = 0;
         for (int m = lane; m < k; m += 32) sum += pair_span(p, q, m).cost();
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -340,6 +340,33 @@ __device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity, uns
     }
 }
 
+// Rows that came out infinite or NaN, of the pairs that this CTA has computed whole:
+// its line from cost unit `at` of pair (s, h, m) on. Warp `warp` of `warps`.
+template <int D, bool I8>
+__device__ __noinline__ void rows_again(const AttnParams &p, int s, int h, int m, int at, long long left, int warp, int warps) {
+    const int lane = threadIdx.x & 31;
+    Walk w;
+    w.s = s;
+    w.h = h;
+    w.m = m;
+    w.load(p);
+    while (left > 0) {
+        const int used = (int)min((long long)(w.a.cost() - at), left);
+        if (at <= kPairCost && at + used == w.a.cost())
+            for (int x = warp; x < w.a.rows; x += warps) {
+                const int r = w.m * kPair + x, tok = group_div(p, r), hq = w.h * p.G + r - tok * p.G;
+                const uint16_t *o = p.out + (w.r.t0 + tok) * p.o_t + hq * p.o_h;
+                bool finite = true;
+#pragma unroll
+                for (int d = 0; d < D; d += 32) finite &= (o[d + lane] & 0x7F80u) != 0x7F80u;
+                if (!__all_sync(0xFFFFFFFFu, finite)) row_again<D, I8>(p, w.s, w.h, w.r.t0, w.r.n, w.r.len, r);
+            }
+        left -= used;
+        at = 0;
+        if (left > 0) w.next(p);
+    }
+}
+
 // ------------------------------------------------------------------ the kernel
 template <int D, bool I8>
 __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
@@ -385,7 +412,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             mbar_init(&ctl->seg_full[i], 1);
             mbar_init(&ctl->seg_empty[i], S::SOFTMAX + 1 + S::LOADERS / 32);
         }
-        ctl->abort = 0;
+        ctl->abort = ctl->again = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // ---- this CTA's piece of the line: warp w sums rows [w per, (w + 1) per)
@@ -418,8 +445,8 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             RowSpan r = {0, 0, 0};
             bool bad = false;
             if (s0 + lane < sb) r = row_span(p, s0 + lane, &bad);
-            const int nb = row_cost(p, r, lane);
-            long long x = (long long)nb * c.nkv;
+            const long long nb = row_cost(p, r, lane);
+            long long x = nb * c.nkv;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
@@ -428,14 +455,14 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             const uint32_t in = __ballot_sync(0xFFFFFFFFu, begin < at + x);
             if (in) {
                 const int src = __ffs(in) - 1;
-                const int row_nb = __shfl_sync(0xFFFFFFFFu, nb, src);
-                const long long row_at = at + __shfl_sync(0xFFFFFFFFu, x, src) - (long long)row_nb * c.nkv;
+                const long long row_nb = __shfl_sync(0xFFFFFFFFu, nb, src);
+                const long long row_at = at + __shfl_sync(0xFFFFFFFFu, x, src) - row_nb * c.nkv;
                 RowSpan q;
                 q.t0 = 0;
                 q.n = __shfl_sync(0xFFFFFFFFu, r.n, src);
                 q.len = __shfl_sync(0xFFFFFFFFu, r.len, src);
                 const int h = (int)((begin - row_at) / row_nb);
-                long long pos = row_at + (long long)h * row_nb;
+                long long pos = row_at + h * row_nb;
                 const int np = pairs_of(p, q);
                 for (int m0 = 0; m0 < np; m0 += 32) {
                     int k = m0 + lane < np ? pair_span(p, q, m0 + lane).cost() : 0, y = k;
@@ -506,10 +533,11 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
             };
             // in cost units: where the work begins in its first pair, how much there is. Of a pair
             // that begins at unit 0, units kPairCost + b are block b.
-            int at = (int)(begin - ctl->seg_at), left = (int)(end - begin);
+            int at = (int)(begin - ctl->seg_at);
+            long long left = end - begin;
             bool first = true;
             while (left > 0) {
-                const int used = min(w.a.cost() - at, left), b0 = max(0, at - kPairCost), b1 = max(0, at + used - kPairCost);
+                const int used = (int)min((long long)(w.a.cost() - at), left), b0 = max(0, at - kPairCost), b1 = max(0, at + used - kPairCost);
                 if (b0 < b1) {
                     if (!slot_free()) break;
                     Seg &g = ctl->seg[k % kSegRing];
@@ -764,7 +792,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                 seg_end(sg);
             }
         };
-        // ================================================ softmax, half a query row a thread
+        // ================================================ softmax, a query row (or half of one) a thread
         if (I8 && warp >= S::LOADER) {
             regs_down<S::REG_LOAD>();
             loader();
@@ -981,8 +1009,8 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                 l += exchange(4, l, 0.f);
                 if (!ok) break;
                 if (b0 == 0 && b1 == g.nb) {
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
-                    float sum = l;
+                    const float inv = l == 0.f ? 0.f : l < INFINITY ? 1.f / l : l - l;  // (a sum beyond FP32: NaN)
+                    float sum = 0.f;
 #pragma unroll 1
                     for (int d = 0; d < DW; d += 16) {
                         uint32_t o[16];
@@ -1010,13 +1038,7 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                         __syncwarp();
                     }
                     fence_before();
-                    uint32_t again = __ballot_sync(0xFFFFFFFFu, row < rows && !(sum < INFINITY));
-                    while (again) {
-                        const int src = __ffs(again) - 1;
-                        again &= again - 1;
-                        // only this half's dimensions: the other half's warp sees to its own
-                        row_again<D, I8>(p, g.s, g.h, g.t0, g.n, g.len, r0 + 32 * (warp & 3) + src, DW * half, DW * half + DW);
-                    }
+                    if (row < rows && !(sum < INFINITY)) ctl->again = 1;
                 } else {
                     // with the sum's powers of two in the reference, so that the join's factors are those of
                     // the weights themselves, however far the reference has lagged
@@ -1078,6 +1100,9 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
     }
+    // ---- rows that came out infinite or NaN, now that no role waits for another
+    if (begin < end && ctl->again && !ctl->abort && warp < S::SOFTMAX)
+        rows_again<D, I8>(p, ctl->seg_s, ctl->seg_h, ctl->seg_m, (int)(begin - ctl->seg_at), end - begin, warp, S::SOFTMAX);
 }
 
 // Adds up the states of the pair that CTA blockIdx.x began, 32 of its query rows a
