@@ -568,9 +568,9 @@ tiles_status_t tiles_paged_append(const tiles_paged_cache *cache, int32_t layer,
  * Positions that it does not see (behind the end, masked, missing pages) have
  * no influence, whatever their bytes. Query head h reads KV head h / (n_q_heads
  * / n_kv_heads); up to 16 query heads a KV head. q, out: BF16, strides as for
- * append (out must not overlap q). max_tokens: a bound on n_s (a row with more
- * is recorded as TILES_ERR_DEVICE_BOUNDS and skipped). Softmax statistics and
- * sums are FP32.
+ * append (out must not overlap q, nor its rows one another). max_tokens: a bound
+ * on n_s (a row with more is recorded as TILES_ERR_DEVICE_BOUNDS and skipped).
+ * Softmax statistics and sums are FP32.
  * workspace: device, 16-byte aligned, tiles_paged_workspace_bytes of it, any
  * contents; calls that overlap in time must not share it. Errors also:
  * CAPACITY (workspace too small). */
@@ -580,8 +580,8 @@ tiles_status_t tiles_paged_attention(const tiles_paged_cache *cache, int32_t lay
                                      int32_t n_tokens, int32_t max_tokens, float scale, int32_t window,
                                      int32_t sinks, void *workspace, int64_t workspace_bytes, void *stream);
 
-/* Workspace of tiles_paged_attention for up to n_tokens tokens, on the current
- * device. Errors: as tiles_paged_get_layout, CUDA. */
+/* Workspace of tiles_paged_attention for rows of up to max_tokens tokens (and so
+ * of fewer), on the current device. Errors: as tiles_paged_get_layout, CUDA. */
 tiles_status_t tiles_paged_workspace_bytes(const tiles_paged_desc *desc, int32_t n_q_heads, int32_t max_tokens,
                                            int64_t *bytes);
 

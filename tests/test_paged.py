@@ -89,6 +89,7 @@ def test_caches_that_are_refused_by_every_call(bad):
     (dict(o_h=63), INVALID), (dict(cu=FAKE + 2), INVALID), (dict(cu=None, n=4), INVALID), (dict(n=-1), INVALID),
     (dict(mx=0), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(ws=None), INVALID),
+    (dict(o_t=0), INVALID), (dict(o_h=56), INVALID),                              # rows of out that overlap
     (dict(ws=FAKE + 4), INVALID), (dict(n=0), OK),                                # nothing to do: no CUDA call either
 ])
 def test_attention_arguments(bad, status):
