@@ -481,7 +481,8 @@ tiles_status_t tiles_kv8_from_bf16(const tiles_model_desc *desc, const void *k_b
  *           all scores of a query alike).
  * The calls read lens, tables and the reference counts on the device: none
  * synchronises, none allocates, and all can be captured into a graph. Calls on
- * one cache must be ordered (one stream, or events). Device-side faults (a page
+ * one cache must be ordered (one stream, or events); attention only reads it, so
+ * that calls of attention with workspaces of their own may overlap. Device-side faults (a page
  * id out of range, too few free pages, a bad row) are recorded in the state's
  * status word; the access is skipped.
  */

@@ -860,3 +860,37 @@ def test_a_tile_of_rows_beside_an_infinity_in_a_long_cache(tsp, d, i8):
                                         [c.values[0][:32641 + tok]], [32641 + tok], np.array([0, 1]), d ** -0.5)
         tol = R.BF16_HALF * np.abs(ref) + (2.0 ** -8 + 2.0 ** -20 + serr) * spread + 1e-30
         assert (np.abs(got[tok] - ref[0]) <= tol[0]).all(), tok
+
+
+def test_one_cache_captured_and_on_two_streams(tsp):
+    """Attention reads a cache only, so calls on it may overlap: eager ones on two streams
+    and a replayed graph on a third have workspaces of their own (none is given here)."""
+    import torch
+    for ns in ([1] * 6, [40, 9, 30, 1, 0, 25]):
+        c = Case(tsp, [700, 40, 1500, 333, 64, 2000], ns, 8, 2, 64, 16, seed=64)
+        want = c.run()
+        c.check(want, weights=2.0 ** -8)
+        q2 = c.q.flip(0).contiguous()
+        want2 = c.run(q=q2)
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        graph, held = torch.cuda.CUDAGraph(), torch.empty_like(want)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=streams[2]):
+            c.run(out=held)
+        outs = [torch.empty_like(want) for _ in range(2)]
+        for _ in range(20):
+            held.zero_()
+            torch.cuda.synchronize()
+            for _ in range(4):
+                with torch.cuda.stream(streams[2]):
+                    graph.replay()
+                for k in range(2):
+                    with torch.cuda.stream(streams[k]):
+                        c.run(out=outs[k], q=(c.q, q2)[k])
+            torch.cuda.synchronize()
+            assert torch.equal(held, want) and torch.equal(outs[0], want) and torch.equal(outs[1], want2)
+        # a larger need on the same stream, then the small one again
+        c.run(max_tokens=40)
+        assert torch.equal(c.run(), want)
+        assert len(c.cache._ws) <= 3
+        c.cache.check()

@@ -299,7 +299,7 @@ class PagedKV:
     ``resize`` gives and takes pages, ``fork`` shares a row's, ``trim`` drops what
     a window no longer sees, ``compact`` closes gaps; ``append`` writes a layer's
     new K/V rows and ``attention`` reads them. All run on the device and can be
-    captured; order them on one stream. ``check`` raises on what they recorded
+    captured; order them on one stream (calls of ``attention`` may overlap). ``check`` raises on what they recorded
     there (a bad page, too few pages).
 
     ``k``, ``v``, ``tables``, ``lens``: existing CUDA buffers to use as they are
@@ -347,10 +347,11 @@ class PagedKV:
             ("k", self.k), ("v", self.v), ("tables", self.tables), ("lens", self.lens), ("state", self.state),
             ("k_shift", k_shift))})
         self._ref = ctypes.byref(self._view)
-        self._ws_bytes = {}
+        self._ws_bytes, self._ws = {}, {}
         self._index, self._d, self._n_cu = self.device.index, d.head_dim, n_seqs + 1
         self._i32, self._bf16, self._u8, self._empty = torch.int32, torch.bfloat16, torch.uint8, torch.empty
         self._device_of, self._stream_of = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        self._capturing = torch._C._cuda_isCurrentStreamCapturing
         self._scale, self._L = d.head_dim ** -0.5, _lib()
 
     def _values(self, buf, off: int):
@@ -451,8 +452,10 @@ class PagedKV:
         """out = softmax attention of the queries q (BF16 CUDA tensor [tokens][n_q_heads][head_dim]; out
         likewise) over their rows' positions up to their own, within `window` (0: all) and the first
         `sinks`. cu_tokens as for append; max_tokens: a bound on a row's tokens; scale: default
-        head_dim ** -0.5. workspace: a uint8 CUDA tensor of workspace_bytes (default: one is taken from
-        PyTorch's allocator for the call)."""
+        head_dim ** -0.5. workspace: a uint8 CUDA tensor of workspace_bytes. Without one the cache keeps
+        one for each stream that such calls are made on (calls on one stream run in order; a call of
+        14 us takes 8 this way); a call that is being captured, or whose stream is an argument, takes
+        its own from PyTorch's allocator."""
         (n, heads, _), qs = self._heads(q, "tiles_paged_attention")
         shape, os_ = self._heads(out, "tiles_paged_attention")
         if shape[0] != n or shape[1] != heads:
@@ -461,19 +464,26 @@ class PagedKV:
         if workspace is None:
             need = self._ws_bytes.get((heads, max_tokens)) or self.workspace_bytes(heads, max_tokens)
             if stream is None:
-                workspace = self._empty(need, dtype=self._u8, device=self.device)
+                capturing = self._capturing()
+                have, ws, _ = (0, 0, None) if capturing else self._ws.get(st, (0, 0, None))
+                if have < need:
+                    workspace = self._empty(need, dtype=self._u8, device=self.device)
+                    have, ws = need, workspace.data_ptr()
+                    if not capturing:
+                        self._ws[st] = have, ws, workspace
             else:
                 import torch
                 with torch.cuda.stream(stream):
                     workspace = self._empty(need, dtype=self._u8, device=self.device)
+                have, ws = need, workspace.data_ptr()
         elif workspace.get_device() != self._index or not workspace.is_contiguous():
             raise TilesError(-1, "tiles_paged_attention: the workspace is contiguous, on the cache's device")
         else:
-            need = workspace.numel() * workspace.element_size()
+            have, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
         _check(self._L.tiles_paged_attention(
             self._ref, layer, heads, q.data_ptr(), qs[0], qs[1], out.data_ptr(), os_[0], os_[1],
             self._cu(cu_tokens, "tiles_paged_attention"), n, max_tokens, self._scale if scale is None else scale, window,
-            sinks, workspace.data_ptr(), need, st), "tiles_paged_attention")
+            sinks, ws, have, st), "tiles_paged_attention")
 
     def status(self, stream=None) -> int:
         """Synchronises and returns (and clears) what the calls recorded on the device."""
