@@ -299,8 +299,8 @@ class PagedKV:
     ``resize`` gives and takes pages, ``fork`` shares a row's, ``trim`` drops what
     a window no longer sees, ``compact`` closes gaps; ``append`` writes a layer's
     new K/V rows and ``attention`` reads them. All run on the device and can be
-    captured; order them on one stream (calls of ``attention`` may overlap). ``check`` raises on what they recorded
-    there (a bad page, too few pages).
+    captured; order them on one stream (calls of ``attention`` may overlap).
+    ``check`` raises on what they recorded there (a bad page, too few pages).
 
     ``k``, ``v``, ``tables``, ``lens``: existing CUDA buffers to use as they are
     (pools of the layout's size; tables int32 [n_seqs][table_width]; lens int32

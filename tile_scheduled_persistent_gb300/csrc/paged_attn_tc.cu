@@ -974,13 +974,14 @@ __global__ void __launch_bounds__(TcShape<D, I8>::THREADS, 1)
                             unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), sc2, nb2), e0, e1);
                             e0 = ex2(e0);
                             e1 = ex2(e1);
-                            ls[j & 1] = add2(ls[j & 1], pack2(e0, e1));
+                            const uint64_t both = pack2(e0, e1);
                             if constexpr (I8) {
                                 const float2 f = *reinterpret_cast<const float2 *>(vs + k);
                                 e0 *= f.x;
                                 e1 *= f.y;
                             }
                             pk[j] = cvt_bf2(e0, e1);
+                            ls[j & 1] = add2(ls[j & 1], both);
                         }
                         tst16(p_tm + 16 * q, pk);
                     }
