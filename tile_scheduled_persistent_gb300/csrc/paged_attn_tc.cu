@@ -37,9 +37,9 @@
 // timeout, lets its copies and MMAs finish (bounded too), frees its tensor memory
 // and returns.
 //
-// Measured on GB300: a prompt of 4,096 (D 128, 32/8 heads, pages of 64) 127 us with the
-// join, 1,078 TFLOP/s, 0.57 of the measured dense BF16 rate; 256 tokens at 32,768 (D 64)
-// 86 us, 0.42; INT8 pages 262 and 154 us. A block of both tiles takes 3,000 cycles at
+// Measured on GB300: a prompt of 4,096 (D 128, 32/8 heads, pages of 64) 128 us with the
+// join, 1,075 TFLOP/s, 0.56 of the measured dense BF16 rate; 256 tokens at 32,768 (D 64)
+// 84 us, 0.43; INT8 pages 262 and 154 us. A block of both tiles takes 3,000 cycles at
 // D 128, of which the tensor cores need 2,048; at D 64 2,800 of 1,024, there the softmax
 // is the longer part.
 #include <cuda.h>
