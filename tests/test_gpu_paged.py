@@ -894,3 +894,51 @@ def test_one_cache_captured_and_on_two_streams(tsp):
         assert torch.equal(c.run(), want)
         assert len(c.cache._ws) <= 3
         c.cache.check()
+
+
+@pytest.mark.parametrize("i8", [False, True])
+def test_pages_behind_four_billion_elements(tsp, i8):
+    """The pool's last pages, whose offsets pass 32 bits: taken, written, read by both kinds
+    of attention, copied on write, and moved to the front."""
+    import torch
+    P, hkv, d, page, lens = 34000, 8, 128, 128, [300, 131]
+    desc = tsp.ModelDesc(n_layers=1, n_q_heads=2 * hkv, n_kv_heads=hkv, head_dim=d, max_pos=512)
+    c = tsp.PagedKV(desc, n_pages=P, page_size=page, n_seqs=3, kv_format=tsp.KV_INT8 if i8 else tsp.KV_BF16)
+    assert (P - 40) * hkv * page * d > 2 ** 32
+    c.refs[:P - 40] = 1                                     # so that only the last pages are free
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    c.resize(dev(lens + [0]))
+    n = sum(lens)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    k, v = (torch.randn((n, hkv, d), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    c.append(0, k, v, cu_tokens=dev([0, lens[0], n, n]))
+    assert int(c.tables.max()) < P and int(c.tables[c.tables >= 0].min()) >= P - 40
+    q = torch.randn((40, 2 * hkv, d), device="cuda", generator=g).to(torch.bfloat16)
+    out1, out2 = torch.zeros_like(q[:3]), torch.zeros_like(q)
+    c.attention(0, q[:3], out1)
+    c.attention(0, q, out2, cu_tokens=dev([0, 30, 40, 40]), max_tokens=30)
+    kk, vv = k.double().cpu().numpy(), v.double().cpu().numpy()
+    if i8:
+        (kc, ks), (vc, vs) = quantized(k.float().cpu().numpy()), quantized(v.float().cpu().numpy())
+        kk, vv = kc * ks[..., None].astype(np.float64), vc * vs[..., None].astype(np.float64)
+    keys, values = [kk[:300], kk[300:]], [vv[:300], vv[300:]]
+    qd = q.double().cpu().numpy()
+    for out, cu, w in ((out1, [0, 1, 2], 2.0 ** -11 if i8 else 2.0 ** -16), (out2, [0, 30, 40], 2.0 ** -8)):
+        ref, spread, serr = R.attention(qd[:cu[-1]], keys, values, lens, np.array(cu), d ** -0.5)
+        err = np.abs(out.double().cpu().numpy()[:cu[-1]] - ref)
+        assert (err <= R.BF16_HALF * np.abs(ref) + (w + 2.0 ** -20 + serr) * spread).all()
+    c.fork(dev([-1, -1, 0]))
+    c.resize(dev([301, -1, 301]))                           # one of the two copies the page it writes
+    c.append(0, k[:2], v[:2], cu_tokens=dev([0, 1, 1, 2]))
+    (kp, _), _ = c.key_pool(), c.value_pool()
+    a, b = int(c.tables[0, 2]), int(c.tables[2, 2])
+    assert a != b and min(a, b) >= P - 40 and torch.equal(kp[0, a, :, :44], kp[0, b, :, :44])
+    before = torch.zeros_like(q[:3])
+    c.attention(0, q[:3], before)
+    c.refs[:P - 40] = 0
+    c.compact()
+    assert int(c.tables.max()) < 40
+    after = torch.zeros_like(before)
+    c.attention(0, q[:3], after)
+    assert torch.equal(before, after)
+    c.check()
